@@ -288,6 +288,124 @@ int w4a4_linear_fused_lora(const uint16_t* x, int64_t ldx, const int8_t* Wq, con
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Element types of the 16-bit tensors of the entries below.
+ */
+#define W4A4_BF16 0
+#define W4A4_FP16 1
+
+/*
+ * Offline weight preparation for w4a4_linear_w4a16: 4-bit codes with one
+ * scale (and one offset) per group of `group` consecutive columns of a row,
+ * no rotation.  The pages have no counterpart to this entry point.
+ *   W       [N, K] fp32, row stride ldw >= K (elements), 16-byte aligned, ldw % 4 == 0
+ *   group   in {32, 64, 128};  N >= 1;  K % 32 == 0, K % group == 0, K <= 131072
+ *   dtype   W4A4_BF16 or W4A4_FP16: the type of scale and offset
+ *   Wq      [N, K/2] int8 output, contiguous rows, the even column in the low
+ *           nibble (the container of w4a4_quantize_weight)
+ *   scale   [N, K/group] output
+ *   offset  [N, K/group] output, or NULL for symmetric codes
+ * Symmetric: s = round16(amax / 7), q = clamp(rne(w / s), -7, 7).  With
+ * offsets: s = round16((max - min) / 15), o = round16(min + 8 s),
+ * q = clamp(rne((w - o) / s), -8, 7).  s = 0 gives q = 0.  The weight that
+ * the codes stand for is s q (+ o).
+ */
+int w4a4_quantize_weight_w4a16(const float* W, int64_t N, int64_t K, int64_t ldw, int group, int dtype,
+                               int8_t* Wq, void* scale, void* offset, void* stream);
+
+/*
+ * Linear layer of a few 16-bit activation rows with 4-bit weights and group
+ * scales (the matrix-vector products of a block: modulation projections,
+ * decode steps), for rows whose own rounding to int4 would cost accuracy and
+ * save nothing:
+ *     y[m, n] = round16( sum_k x[m, k] (scale[n, k/group] q[n, k] + offset[n, k/group]) + bias[n] )
+ * with products and sums in fp32.  The pages have no counterpart to this
+ * entry point.
+ *   x [M, K] dtype, row stride ldx >= K, ldx % 8 == 0, 16-byte aligned
+ *   Wq [N, K/2] int8 (16-byte aligned), scale / offset [N, K/group] dtype
+ *       (offset may be NULL), bias [N] dtype or NULL: contiguous, from
+ *       w4a4_quantize_weight_w4a16 or any other quantiser; all 16 codes of a
+ *       nibble are valid (two's complement, -8..7)
+ *   y [M, N] dtype output, row stride ldy >= N (no alignment rule)
+ *   0 <= M <= 64 (M == 0 is a no-op), N >= 1, 32 <= K <= 131072, K % 32 == 0,
+ *   K % group == 0, group in {32, 64, 128}
+ * The result does not depend on what else runs (no atomics); a row's result
+ * does not depend on the other rows' values.
+ */
+int w4a4_linear_w4a16(const void* x, int64_t ldx, const int8_t* Wq, const void* scale, const void* offset,
+                      int group, const void* bias, void* y, int64_t ldy, int64_t M, int64_t N, int64_t K, int dtype,
+                      void* stream);
+
+/*
+ * RMS norm of every query and key head and the rotary rotation of both in
+ * one pass over them, with positions on several axes (one for text; height
+ * and width for images; time, height and width for video).  For each token t
+ * and head, over the D elements h of the head:
+ *     u = h / sqrt(mean(h^2) + eps) * weight           (weight NULL: u = h)
+ *     angle_i = positions[t, axis[i]] * freq[i],  i < R/2
+ *     interleaved:  (u_2i, u_2i+1)     turned by angle_i
+ *     else:         (u_i,  u_i + R/2)  turned by angle_i
+ * (a, b) turned by t is (a cos t - b sin t, a sin t + b cos t).  Elements R..D-1 are
+ * not turned.  Norm and rotation are formed in fp32 (the angle's reduction in
+ * fp64, so far positions keep their precision) and rounded once.  The pages
+ * have no counterpart to this entry point.
+ *   q [T, Hq, D], k [T, Hk, D] dtype; token and head strides in elements,
+ *       multiples of 8, 16-byte aligned, D contiguous.  Hk == 0: no keys.
+ *   q_weight, k_weight [D] dtype, 16-byte aligned, or NULL for no norm of q / of k
+ *   positions [T, axes] int32 (position_bits 32) or int64 (64), row stride
+ *       pos_stride; or NULL for no rotation (R, freq and axis are then ignored)
+ *   freq [R/2] fp64 (radians per position), axis [R/2] int32 (values outside
+ *       0..axes-1 are clamped into it); 1 <= axes <= 8
+ *   q_out [T, Hq, D], k_out [T, Hk, D]: rules as for q and k; may be q and k
+ *       themselves (same pointer and strides), otherwise no overlap
+ *   T >= 0; D % 8 == 0, 8 <= D <= 256; R even, 2 <= R <= D, R % 16 == 0 unless
+ *       interleaved;  Hq >= 1, Hq + Hk <= 4096;  eps >= 0, finite
+ */
+int w4a4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t Hq, const void* k,
+                      int64_t k_token_stride, int64_t k_head_stride, int64_t Hk, const void* q_weight,
+                      const void* k_weight, float eps, const void* positions, int position_bits, int64_t pos_stride,
+                      int axes, const double* freq, const int32_t* axis, int64_t R, int interleaved, void* q_out,
+                      int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                      int64_t k_out_token_stride, int64_t k_out_head_stride, int64_t T, int64_t D, int dtype,
+                      void* stream);
+
+/*
+ * Softmax attention over packed sequences.  Sequence b has query rows
+ * cu_q[b] .. cu_q[b+1]-1 (Lq of them) and key rows cu_k[b] .. cu_k[b+1]-1 (Lk).
+ * Query i of it sees key j when j < Lk and, if causal, j <= i + Lk - Lq (the last query
+ * sees every key: a prompt, its tail over a cache, or a single token).  With
+ * s_j = scale * q_i . k_j over the keys it sees and head h reading key head
+ * h / (Hq / Hk):
+ *     lse = log sum_j exp(s_j),   out = round16( sum_j exp(s_j - lse) v_j )
+ * A query that sees nothing gets out = 0 and lse = -inf.  The pages have no
+ * counterpart to this entry point.
+ *   q [Tq, Hq, D], k [Tk, Hk, D], v [Tk, Hk, D] dtype; token and head strides
+ *       in elements, multiples of 8, 16-byte aligned, D contiguous
+ *   out [Tq, Hq, D] dtype, rules as for q, no overlap with the inputs
+ *   lse [Tq, Hq] fp32 contiguous, or NULL
+ *   cu_q, cu_k [B + 1] int32 on the device, non-decreasing from 0 (values are
+ *       clamped into [0, T] and a negative length is taken as 0, so that a
+ *       bad array reads and writes nothing out of range); both NULL with
+ *       B == 1: one sequence of all the rows
+ *   Rows of out and lse behind the last sequence keep what they hold.
+ *   D in {64, 128}; Hq % Hk == 0; 1 <= Hq <= 65535; scale finite and > 0;
+ *   0 <= Tq, Tk <= 2^30, B >= 1
+ *   workspace: w4a4_attention_workspace_bytes(...) bytes of the same sizes
+ *       (0 for most), 256-byte aligned, no initialisation needed.  Calls that
+ *       may overlap on the GPU need workspaces of their own.
+ * Key and value rows outside a query's sequence never reach it, whatever they
+ * hold.  Inside a sequence a NaN or an infinity among the values may reach
+ * queries that the causal rule keeps from seeing it (its weight 0 times the
+ * value), none other.
+ */
+size_t w4a4_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk, int64_t D);
+int w4a4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                   int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                   int64_t v_head_stride, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                   const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
+                   int64_t Hk, int64_t D, int causal, float scale, int dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the device status word that
  * kernels set when a bounded wait expires.  Returns W4A4_OK,
  * W4A4_ERR_TIMEOUT, or W4A4_ERR_CUDA if the synchronisation failed.

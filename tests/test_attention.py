@@ -1,0 +1,322 @@
+"""attention against its definition in float64.
+
+Bound per element of `out`, with p_j the exact weights of the keys a query
+sees, L their number, S = scale max_j sum_d |q_d k_jd|:
+  * scores: D products summed in fp32 (a matrix unit may truncate where an
+    adder rounds: 2^-23 a step), the scale and the shift by the maximum:
+    off by at most ds = (D + 8) 2^-23 S + 2^-20, the last term the
+    exponential's own error; weights are off by 2 ds relative (numerator and sum);
+  * weights rounded to 16 bits before they meet v: eps/2 relative, and in fp16
+    below 2^-14 half a subnormal step, 2^-25 (the sum they are divided by is at least 1);
+  * sums of L terms in fp32: L 2^-23 relative to sum_j p_j |v_j|;
+  * the output's own rounding: eps/2.
+lse: ds + L 2^-23 + 2^-20 (1 + |lse|)."""
+
+import math
+
+import pytest
+import torch
+
+import w4a4_hadamard_rotated_b200 as w4
+
+DTYPES = [torch.bfloat16, torch.float16]
+
+
+def cu(lengths):
+    return torch.tensor([sum(lengths[:i]) for i in range(len(lengths) + 1)], dtype=torch.int32, device="cuda")
+
+
+def make(Tq, Tk, Hq, Hk, D, dtype, seed=0, spread=1.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: (torch.randn(*s, generator=gen, device="cuda") * spread).to(dtype)
+    return r(Tq, Hq, D), r(Tk, Hk, D), r(Tk, Hk, D)
+
+
+def check(out, lse, q, k, v, qs, ks, causal, scale=None):
+    """Every row of the packed result against float64 (on the GPU, one
+    sequence and head group at a time)."""
+    Hq, D = q.shape[1:]
+    G = Hq // k.shape[1]
+    scale = D ** -0.5 if scale is None else scale
+    eps = torch.finfo(q.dtype).eps
+    q0 = k0 = 0
+    for n, m in zip(qs, ks):
+        for h in range(Hq):
+            qq, kk, vv = q[q0:q0 + n, h].double(), k[k0:k0 + m, h // G].double(), v[k0:k0 + m, h // G].double()
+            o, z = out[q0:q0 + n, h].double(), lse[q0:q0 + n, h].double()
+            seen = torch.ones(n, m, dtype=torch.bool, device="cuda")
+            if causal:
+                seen = torch.arange(m, device="cuda") <= torch.arange(n, device="cuda")[:, None] + (m - n)
+            s = (qq @ kk.t() * scale).masked_fill(~seen, -math.inf)
+            top = s.amax(1, keepdim=True) if m else torch.full((n, 1), -math.inf, device="cuda", dtype=torch.float64)
+            p = (s - torch.where(top == -math.inf, 0.0, top)).exp()
+            total = p.sum(1, keepdim=True)
+            rows = (total > 0)[:, 0]
+            assert (o[~rows] == 0).all() and (z[~rows] == -math.inf).all()
+            if not rows.any():
+                continue
+            p = (p / total.clamp(min=1e-300))[rows]
+            ref, A = p @ vv, p @ vv.abs()
+            L = seen[rows].sum(1, keepdim=True).double()
+            S = ((qq.abs() @ kk.abs().t()) * scale * seen).amax(1, keepdim=True)[rows]
+            ds = (D + 8) * 2.0 ** -23 * S + 2.0 ** -20
+            tol = eps / 2 * ref.abs() + (eps / 2 + 2 * ds + L * 2.0 ** -23) * A * (1 + eps) + 2.0 ** -25
+            if q.dtype == torch.float16:
+                tol = tol + 2.0 ** -25 * (seen[rows].double() @ vv.abs())
+            bad = ~((o[rows] - ref).abs() <= tol)
+            assert not bad.any(), (f"sequence {n}x{m} head {h}: {int(bad.sum())} of {bad.numel()} off, first at "
+                                   f"{bad.nonzero()[0].tolist()}, worst {((o[rows] - ref).abs() / tol).max():.3g} of the bound")
+            want = (top + total.log())[rows]
+            off = (z[rows][:, None] - want).abs()
+            assert (off <= ds + L * 2.0 ** -23 + 2.0 ** -20 * (1 + want.abs())).all(), f"lse of {n}x{m} head {h}: {off.max():.3g}"
+        q0, k0 = q0 + n, k0 + m
+
+
+def go(qs, ks, Hq, Hk, D, dtype, causal, seed=0, spread=1.0, scale=None):
+    q, k, v = make(sum(qs), sum(ks), Hq, Hk, D, dtype, seed, spread)
+    out, lse = w4.attention(q, k, v, cu(qs), cu(ks), causal=causal, scale=scale, return_lse=True)
+    assert out.shape == q.shape and out.dtype == dtype
+    check(out, lse, q, k, v, qs, ks, causal, scale)
+    assert w4.last_device_error() == 0
+    return q, k, v, out, lse
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("n", [1, 2, 31, 64, 127, 128, 129, 200, 255, 256, 257, 385, 513, 1000])
+def test_one_prompt(cuda_lib, dtype, D, causal, n):
+    go([n], [n], 2, 1, D, dtype, causal, seed=n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (3, 3), (6, 2), (5, 1), (8, 1), (16, 2), (12, 3), (32, 1), (7, 7)])
+def test_packed_prompts_and_heads(cuda_lib, D, causal, Hq, Hk):
+    n = [300, 1, 0, 77, 128, 257, 33]
+    go(n, n, Hq, Hk, D, torch.bfloat16, causal, seed=Hq)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("qs,ks", [
+    ([1], [5000]),                                  # one token over a cache
+    ([1, 1, 1, 1], [4097, 1, 300, 129]),
+    ([3, 1, 2], [2000, 64, 5]),                     # a few tokens
+    ([17, 130], [1000, 131]),                       # the tail of a prompt
+    ([5, 200, 1], [3, 150, 0]),                     # more queries than keys: causal rows that see nothing
+    ([4, 0, 6], [0, 9, 0]),                         # no keys; no queries
+    ([1], [1]),
+    ([300], [40]),
+])
+def test_lengths_of_queries_and_keys_differ(cuda_lib, dtype, causal, qs, ks):
+    go(qs, ks, 8, 2, 128, dtype, causal, seed=sum(ks))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk,D", [(32, 8, 128), (5, 5, 64), (25, 5, 128), (64, 1, 64)])
+def test_single_tokens_over_long_caches(cuda_lib, Hq, Hk, D):
+    ks = [20000, 1, 129, 8192, 777]
+    go([1] * 5, ks, Hq, Hk, D, torch.bfloat16, True, seed=Hq)
+
+
+@pytest.mark.gpu
+def test_many_short_sequences(cuda_lib):
+    gen = torch.Generator().manual_seed(1)
+    n = torch.randint(0, 40, (300,), generator=gen).tolist()
+    go(n, n, 2, 2, 64, torch.float16, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+def test_long_prompt(cuda_lib, causal):
+    go([4500], [4500], 2, 2, 128, torch.bfloat16, causal)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("spread,scale", [(8.0, None), (0.01, None), (1.0, 1.0), (1.0, 1e-6), (3.0, 0.5)])
+def test_sharp_and_flat_softmax(cuda_lib, spread, scale):
+    """Scores of hundreds, where the running maximum moves by much from tile to
+    tile, and scores that are all alike."""
+    go([300], [700], 2, 2, 128, torch.bfloat16, False, spread=spread, scale=scale)
+    go([300], [700], 2, 2, 64, torch.float16, True, spread=spread, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_running_maximum_moves_every_tile(cuda_lib, order):
+    """Keys whose score grows (or falls) steadily along the sequence."""
+    q, k, v = make(200, 1500, 2, 2, 128, torch.bfloat16)
+    ramp = torch.linspace(0.0, 8.0, 1500, device="cuda")
+    ramp = ramp if order == "rising" else ramp.flip(0)
+    q[:] = 1
+    k[:] = ramp[:, None, None].to(k.dtype)
+    out, lse = w4.attention(q, k, v, return_lse=True)
+    check(out, lse, q, k, v, [200], [1500], False)
+
+
+@pytest.mark.gpu
+def test_without_lengths_is_one_sequence(cuda_lib):
+    q, k, v = make(333, 444, 4, 2, 128, torch.bfloat16)
+    a = w4.attention(q, k, v)
+    b = w4.attention(q, k, v, cu([333]), cu([444]))
+    assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_strides(cuda_lib, D, causal):
+    """q, k and v out of one fused buffer, held head by head, and an output
+    that is a slice of a wider one."""
+    T, Hq, Hk = 190, 6, 2
+    buf = torch.randn(T, (Hq + 2 * Hk) * D, device="cuda").to(torch.bfloat16)
+    q, k, v = (t.view(T, -1, D) for t in buf.split([Hq * D, Hk * D, Hk * D], 1))
+    want, lse = w4.attention(q.contiguous(), k.contiguous(), v.contiguous(), causal=causal, return_lse=True)
+    check(want, lse, q, k, v, [T], [T], causal)
+    wide = torch.full((T, Hq + 3, D + 8), 5.0, device="cuda", dtype=torch.bfloat16)
+    got = w4.attention(q, k, v, causal=causal, out=wide[:, 1:1 + Hq, :D])
+    assert torch.equal(got, want)
+    assert (wide[:, 0] == 5).all() and (wide[:, 1 + Hq:] == 5).all() and (wide[:, :, D:] == 5).all()
+    major = [t.permute(1, 0, 2).contiguous().permute(1, 0, 2) for t in (q, k, v)]
+    assert torch.equal(w4.attention(*major, causal=causal), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("qs,ks", [([100, 60, 130], [100, 60, 130]), ([1, 1, 1], [700, 130, 2000])])
+def test_rows_outside_the_sequences(cuda_lib, causal, qs, ks):
+    """Rows behind the last sequence keep what they hold, and what is there in
+    q, k and v reaches nothing, NaN and infinities included; nor does one
+    sequence reach another."""
+    Hq, Hk, D = 4, 2, 128
+    q, k, v = make(sum(qs), sum(ks), Hq, Hk, D, torch.bfloat16)
+    want, wl = w4.attention(q, k, v, cu(qs), cu(ks), causal=causal, return_lse=True)
+    pad = lambda t, fill: torch.cat((t, torch.full((37, *t.shape[1:]), fill, device="cuda", dtype=t.dtype)))
+    q2, k2, v2 = pad(q, math.nan), pad(k, math.inf), pad(v, math.nan)
+    out = torch.full_like(q2, 3.0)
+    got, gl = w4.attention(q2, k2, v2, cu(qs), cu(ks), causal=causal, out=out, return_lse=True)
+    assert torch.equal(got[:sum(qs)], want) and torch.equal(gl[:sum(qs)], wl)
+    assert (got[sum(qs):] == 3).all()
+    # the middle sequence all NaN: the others are as they were
+    a, b = ks[0], ks[0] + ks[1]
+    k3, v3 = k.clone(), v.clone()
+    k3[a:b], v3[a:b] = math.nan, math.nan
+    got = w4.attention(q, k3, v3, cu(qs), cu(ks), causal=causal)
+    a, b = qs[0], qs[0] + qs[1]
+    assert torch.equal(got[:a], want[:a]) and torch.equal(got[b:], want[b:])
+    assert torch.isnan(got[a:b]).all()
+
+
+@pytest.mark.gpu
+def test_masked_keys_inside_a_sequence(cuda_lib):
+    """Keys that the causal rule hides may be NaN or infinite."""
+    q, k, v = make(300, 300, 2, 2, 128, torch.bfloat16)
+    want = w4.attention(q, k, v, causal=True)
+    k2 = k.clone()
+    k2[150:] = math.nan
+    got = w4.attention(q, k2, v, causal=True)
+    assert torch.equal(got[:150], want[:150]) and torch.isnan(got[150:]).all()
+    k2[150:] = math.inf
+    got = w4.attention(q, k2, v, causal=True)
+    assert torch.equal(got[:150], want[:150])
+
+
+@pytest.mark.gpu
+def test_nan_queries_stay_in_their_rows(cuda_lib):
+    q, k, v = make(130, 300, 4, 2, 64, torch.float16)
+    want = w4.attention(q, k, v)
+    q2 = q.clone()
+    q2[7, 1] = math.nan
+    got = w4.attention(q2, k, v)
+    keep = torch.ones(130, 4, dtype=torch.bool, device="cuda")
+    keep[7, 1] = False
+    assert torch.equal(got[keep], want[keep]) and torch.isnan(got[7, 1]).all()
+
+
+@pytest.mark.gpu
+def test_lengths_that_do_not_fit_stay_in_range(cuda_lib):
+    """Lengths past the rows, falling ones and negative ones are clamped: rows
+    that no sequence covers keep what they hold."""
+    q, k, v = make(100, 100, 2, 2, 64, torch.bfloat16)
+    bad = torch.tensor([0, 60, 40, 1000], dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 2.0)
+    w4.attention(q, k, v, bad, bad, out=out)
+    first = w4.attention(q[:40], k[:60], v[:60])
+    assert torch.isfinite(out).all() and torch.equal(out[:40], first)
+    neg = torch.tensor([-5, 30, 30, -7], dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 2.0)
+    w4.attention(q, k, v, neg, neg, out=out)
+    assert torch.equal(out[:30], w4.attention(q[:30], k[:30], v[:30])) and (out[30:] == 2).all()
+    assert w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_empty_calls(cuda_lib):
+    q, k, v = make(5, 0, 2, 2, 64, torch.bfloat16)
+    out, lse = w4.attention(q, k, v, return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    q, k, v = make(0, 5, 2, 2, 64, torch.bfloat16)
+    assert w4.attention(q, k, v).shape == (0, 2, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qs,ks", [([1, 1], [3000, 500]), ([300, 40], [300, 40])])
+def test_graphs_streams_and_repeats(cuda_lib, qs, ks):
+    """Deterministic; on a side stream; two captured graphs replayed at once on
+    their own streams with eager calls between; lengths that change on the
+    device between replays."""
+    q, k, v = make(sum(qs), sum(ks), 8, 2, 128, torch.bfloat16)
+    q2 = make(sum(qs), 1, 8, 1, 128, torch.bfloat16, seed=9)[0]
+    cq, ck = cu(qs), cu(ks)
+    want, want2 = (w4.attention(t, k, v, cq, ck, causal=True) for t in (q, q2))
+    assert torch.equal(want, w4.attention(q, k, v, cq, ck, causal=True))
+    bufs = [q.clone(), q2.clone()]
+    graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for b in bufs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(w4.attention(b, k, v, cq, ck, causal=True))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = w4.attention(q, k, v, cq, ck, causal=True)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want2) and torch.equal(eager, want)
+    # the same graph after the sequences' lengths changed in place
+    shorter = cu([ks[0] - 100, ks[1]])
+    ck.copy_(shorter)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], w4.attention(q, k, v, cq, shorter, causal=True))
+
+
+@pytest.mark.gpu
+def test_binding_refusals(cuda_lib):
+    q, k, v = make(4, 6, 4, 2, 64, torch.bfloat16)
+    c = cu([4])
+    bad = [
+        (TypeError, lambda: w4.attention(q.float(), k, v)),
+        (TypeError, lambda: w4.attention(q, k.half(), v)),
+        (TypeError, lambda: w4.attention(q, k, v, c.long(), c.long())),
+        (ValueError, lambda: w4.attention(q, k, v[:5])),
+        (ValueError, lambda: w4.attention(q, k, v, c)),
+        (ValueError, lambda: w4.attention(q, k, v, c, torch.cat((c, c)))),
+        (ValueError, lambda: w4.attention(q, k, v, c[:1], c[:1])),
+        (ValueError, lambda: w4.attention(q[0], k, v)),
+        (ValueError, lambda: w4.attention(q.transpose(1, 2).contiguous().transpose(1, 2), k, v)),
+        (ValueError, lambda: w4.attention(q, k, v, out=torch.empty(4, 4, 32, device="cuda", dtype=q.dtype))),
+        (w4.W4A4Error, lambda: w4.attention(q[:, :3], k, v)),
+        (w4.W4A4Error, lambda: w4.attention(q[..., :32], k[..., :32], v[..., :32])),
+        (w4.W4A4Error, lambda: w4.attention(q, k, v, scale=0.0)),
+        (w4.W4A4Error, lambda: w4.attention(q, k[:, :1].expand(6, 2, 64), v)),
+    ]
+    for kind, call in bad:
+        with pytest.raises(kind):
+            call()

@@ -1,0 +1,105 @@
+"""Refusals of the entries that run between a block's linears: invalid
+arguments come back as status codes before any CUDA call, and the binding
+refuses tensors the library cannot take."""
+
+import ctypes
+
+import pytest
+import torch
+
+import w4a4_hadamard_rotated_b200 as w4
+
+NULL = ctypes.c_void_p(0)
+FAKE = ctypes.c_void_p(1 << 20)          # never dereferenced: every call below fails validation first
+ODD = ctypes.c_void_p((1 << 20) + 2)
+BYTE = ctypes.c_void_p((1 << 20) + 1)
+
+NULL_, SHAPE, GROUP, ALIGN, WORKSPACE, ARG = 1, 2, 3, 4, 5, 9
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return w4.load_library()
+
+
+QUANT = dict(W=FAKE, N=8, K=256, ldw=256, group=64, dtype=0, Wq=FAKE, scale=FAKE, offset=NULL, stream=NULL)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(W=NULL), NULL_), (dict(Wq=NULL), NULL_), (dict(scale=NULL), NULL_), (dict(group=16), GROUP),
+    (dict(group=256), GROUP), (dict(K=96, ldw=96), GROUP), (dict(K=48, ldw=48), SHAPE), (dict(N=0), SHAPE),
+    (dict(K=262144, ldw=262144), SHAPE), (dict(ldw=255), SHAPE), (dict(ldw=258), ALIGN), (dict(W=ODD), ALIGN),
+    (dict(Wq=ODD), ALIGN), (dict(scale=BYTE), ALIGN), (dict(offset=BYTE), ALIGN), (dict(dtype=2), ARG)])
+def test_quantize_weight_w4a16_refuses(lib, change, status):
+    assert lib.w4a4_quantize_weight_w4a16(*{**QUANT, **change}.values()) == status
+
+
+LINEAR = dict(x=FAKE, ldx=256, Wq=FAKE, scale=FAKE, offset=NULL, group=64, bias=NULL, y=FAKE, ldy=9, M=3, N=9, K=256,
+              dtype=0, stream=NULL)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(x=NULL), NULL_), (dict(Wq=NULL), NULL_), (dict(scale=NULL), NULL_), (dict(y=NULL), NULL_),
+    (dict(group=48), GROUP), (dict(K=96, ldx=96), GROUP), (dict(K=0), SHAPE), (dict(K=40), SHAPE), (dict(N=0), SHAPE),
+    (dict(M=-1), SHAPE), (dict(M=65), SHAPE), (dict(ldx=248), SHAPE), (dict(ldy=8), SHAPE), (dict(ldx=260), ALIGN),
+    (dict(x=ODD), ALIGN), (dict(Wq=ODD), ALIGN), (dict(y=BYTE), ALIGN), (dict(bias=BYTE), ALIGN), (dict(dtype=-1), ARG)])
+def test_linear_w4a16_refuses(lib, change, status):
+    assert lib.w4a4_linear_w4a16(*{**LINEAR, **change}.values()) == status
+
+
+ROPE = dict(q=FAKE, qt=512, qh=128, Hq=4, k=FAKE, kt=256, kh=128, Hk=2, qw=FAKE, kw=FAKE, eps=1e-6, pos=FAKE, bits=32,
+            pt=3, axes=3, freq=FAKE, axis=FAKE, R=128, interleaved=1, qo=FAKE, qot=512, qoh=128, ko=FAKE, kot=256,
+            koh=128, T=5, D=128, dtype=0, stream=NULL)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=NULL), NULL_), (dict(k=NULL), NULL_), (dict(ko=NULL), NULL_), (dict(qo=NULL), NULL_),
+    (dict(freq=NULL), NULL_), (dict(axis=NULL), NULL_), (dict(T=-1), SHAPE), (dict(D=100), SHAPE),
+    (dict(D=264), SHAPE), (dict(D=0), SHAPE), (dict(Hq=0), SHAPE), (dict(Hk=-1), SHAPE), (dict(Hq=4090, Hk=8), SHAPE),
+    (dict(R=0), SHAPE), (dict(R=130), SHAPE), (dict(R=63), SHAPE), (dict(R=24, interleaved=0), SHAPE),
+    (dict(axes=0), SHAPE), (dict(axes=9, pt=9), SHAPE), (dict(pt=2), SHAPE), (dict(qt=64), SHAPE), (dict(kh=64), SHAPE),
+    (dict(qot=0), SHAPE), (dict(qt=516), ALIGN), (dict(qoh=132), ALIGN), (dict(q=ODD), ALIGN), (dict(kw=ODD), ALIGN),
+    (dict(pos=ODD), ALIGN), (dict(bits=16), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG),
+    (dict(eps=float("inf")), ARG), (dict(dtype=3), ARG)])
+def test_qk_norm_rope_refuses(lib, change, status):
+    assert lib.w4a4_qk_norm_rope(*{**ROPE, **change}.values()) == status
+
+
+ATTN = dict(q=FAKE, qt=1024, qh=128, k=FAKE, kt=256, kh=128, v=FAKE, vt=256, vh=128, out=FAKE, ot=1024, oh=128, lse=FAKE,
+            cuq=FAKE, cuk=FAKE, B=2, Tq=100, Tk=200, Hq=8, Hk=2, D=128, causal=1, scale=0.1, dtype=0, ws=NULL, wsb=0,
+            stream=NULL)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=NULL), NULL_), (dict(k=NULL), NULL_), (dict(v=NULL), NULL_), (dict(out=NULL), NULL_), (dict(cuq=NULL), NULL_),
+    (dict(cuk=NULL), NULL_), (dict(cuq=NULL, cuk=NULL), NULL_), (dict(B=0), SHAPE), (dict(D=96), SHAPE),
+    (dict(Hk=3), SHAPE), (dict(Hk=0), SHAPE), (dict(Hq=0), SHAPE), (dict(Hq=65536, Hk=1), SHAPE), (dict(Tq=-1), SHAPE),
+    (dict(Tk=2 ** 31), SHAPE), (dict(kt=64), SHAPE), (dict(vh=0), SHAPE), (dict(ot=100), SHAPE), (dict(qt=1028), ALIGN),
+    (dict(v=ODD), ALIGN), (dict(out=ODD), ALIGN), (dict(lse=ODD), ALIGN), (dict(cuq=ODD), ALIGN), (dict(scale=0.0), ARG),
+    (dict(scale=-1.0), ARG), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG), (dict(dtype=2), ARG)])
+def test_attention_refuses(lib, change, status):
+    assert lib.w4a4_attention(*{**ATTN, **change}.values()) == status
+
+
+def test_binding_refuses_host_tensors_and_other_types():
+    h = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    calls = [
+        lambda: w4.quantize_weight_w4a16(torch.zeros(8, 128)),
+        lambda: w4.linear_w4a16(torch.zeros(1, 128, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.int8),
+                                torch.zeros(8, 1, dtype=torch.bfloat16)),
+        lambda: w4.qk_norm_rope(h, h),
+        lambda: w4.attention(h, h, h),
+    ]
+    for call in calls:
+        with pytest.raises(TypeError, match="CUDA tensor"):
+            call()
+
+
+def test_rotary_frequencies():
+    freq, axis = w4.rotary_frequencies((4, 6), theta=100.0, device="cpu")
+    assert freq.dtype == torch.float64 and axis.dtype == torch.int32
+    assert axis.tolist() == [0, 0, 1, 1, 1]
+    assert freq.tolist() == pytest.approx([1.0, 100.0 ** -0.5, 1.0, 100.0 ** (-1 / 3), 100.0 ** (-2 / 3)], rel=1e-15)
+    for bad in ((), (3,), (0, 4), (4, -2)):
+        with pytest.raises(ValueError):
+            w4.rotary_frequencies(bad)

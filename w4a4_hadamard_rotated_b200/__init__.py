@@ -13,6 +13,12 @@ Functions keep the C names without the ``w4a4_`` prefix:
   linear(Xq, sx, Wq, sw, bias=None)          -> y [M, N] bf16
   linear_fused(x, Wq, sw, bias=None, g, act) -> y [M, N] bf16
   gemm_s32(Xq, Wq, path=0)                   -> acc [M, N] int32
+and what a transformer block runs between its linears:
+  quantize_weight_w4a16(W, group)            -> (Wq [N, K/2] int8, scale, offset)
+  linear_w4a16(x, Wq, scale, offset, bias)   -> y [M, N], a few rows in 16 bits
+  rotary_frequencies(axis_dims, theta)       -> (freq [R/2] fp64, axis [R/2] int32)
+  qk_norm_rope(q, k, ...)                    -> (q, k) normed per head and rotated
+  attention(q, k, v, cu_seqlens_q, ...)      -> out [Tq, Hq, D] (and lse)
 """
 
 import ctypes
@@ -56,6 +62,13 @@ SIGNATURES = {
     "w4a4_fused_requant_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "w4a4_linear_fused_requant": (_I, [_P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _I, _P, _P, _P, _SZ,
                                        _P]),
+    "w4a4_quantize_weight_w4a16": (_I, [_P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P]),
+    "w4a4_linear_w4a16": (_I, [_P, _I64, _P, _P, _P, _I, _P, _P, _I64, _I64, _I64, _I64, _I, _P]),
+    "w4a4_qk_norm_rope": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _I, _I64, _I,
+                               _P, _P, _I64, _I, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _P]),
+    "w4a4_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "w4a4_attention": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64,
+                            _I64, _I64, _I64, _I64, _I, ctypes.c_float, _I, _P, _SZ, _P]),
     "w4a4_last_device_error": (_I, [_P]),
     "w4a4_debug_wait_timeout": (_I, [_I64, _P]),
     "w4a4_debug_set_wait_limit": (_I, [_I64]),
@@ -355,6 +368,243 @@ def linear_fused_lora(x, Wq, sw, bias, A, B, scale, g=128, out=None):
                                       float(scale), _ptr(y), y.stride(0), M, N, K, g, _ptr(ws), nbytes,
                                       _stream(x)), "w4a4_linear_fused_lora")
     return y
+
+
+# ---- what a transformer block runs between its linears
+#
+# These entries launch on the current stream of the tensors' own device, also
+# when another device is current.
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}      # W4A4_BF16, W4A4_FP16
+
+
+def _need_16bit(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    return code
+
+
+def _same(t, dtype, shape, name, device):
+    """A contiguous operand of the given type and shape on the device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _call(fn, device, args, what):
+    """fn(*args, stream) with `device` current."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != OK:
+        raise W4A4Error(status, what)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def quantize_weight_w4a16(W, group=128, dtype=torch.bfloat16, asymmetric=False):
+    """Quantise fp32 weights W [N, K] to 4 bits with one scale per `group`
+    columns, for linear_w4a16 -> (Wq [N, K/2] int8, scale [N, K/group] dtype,
+    offset [N, K/group] dtype, or None unless asymmetric)."""
+    lib = load_library()
+    _need_cuda(W, torch.float32, "W")
+    if W.dim() != 2 or W.stride(1) != 1:
+        raise ValueError("W must be a 2-D tensor with a contiguous inner dimension")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+    N, K = W.shape
+    if group not in (32, 64, 128) or K % group != 0:
+        raise ValueError(f"group must be 32, 64 or 128 and divide K = {K}, got {group}")
+    Wq = torch.empty(N, K // 2, dtype=torch.int8, device=W.device)
+    scale = torch.empty(N, K // group, dtype=dtype, device=W.device)
+    offset = torch.empty_like(scale) if asymmetric else None
+    _call(lib.w4a4_quantize_weight_w4a16, W.device,
+          (W.data_ptr(), N, K, W.stride(0), group, _DTYPES[dtype], Wq.data_ptr(), scale.data_ptr(), _addr(offset)),
+          "w4a4_quantize_weight_w4a16")
+    return Wq, scale, offset
+
+
+def linear_w4a16(x, Wq, scale, offset=None, bias=None, out=None):
+    """y [M, N] = x W^T (+ bias) for M <= 64 rows of bf16 or fp16 x [M, K] and
+    4-bit weights W[n, k] = scale[n, k/group] Wq[n, k] (+ offset[n, k/group]);
+    the group is K / scale.shape[1].  scale, offset, bias and y have x's type."""
+    lib = _lib or load_library()
+    code = _need_16bit(x, "x")
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be a 2-D tensor with a contiguous inner dimension")
+    M, K = x.shape
+    dev, dtype = x.device, x.dtype
+    if not isinstance(Wq, torch.Tensor) or Wq.dim() != 2:
+        raise ValueError("Wq must be a contiguous [N, K/2] int8 tensor on x's device")
+    N = Wq.shape[0]
+    _same(Wq, torch.int8, (N, K // 2), "Wq", dev)
+    if not isinstance(scale, torch.Tensor) or scale.dim() != 2 or scale.shape[1] < 1 or K % scale.shape[1] != 0:
+        raise ValueError("scale must be a [N, K/group] tensor")
+    groups = scale.shape[1]
+    _same(scale, dtype, (N, groups), "scale", dev)
+    if offset is not None:
+        _same(offset, dtype, (N, groups), "offset", dev)
+    if bias is not None:
+        _same(bias, dtype, (N,), "bias", dev)
+    if out is None:
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+    else:
+        y = out
+        _need_rows(y, dtype, M, N, "out", dev)
+    _call(lib.w4a4_linear_w4a16, dev,
+          (x.data_ptr(), x.stride(0) if M > 1 else K, Wq.data_ptr(), scale.data_ptr(), _addr(offset), K // groups,
+           _addr(bias), y.data_ptr(), y.stride(0) if M > 1 else N, M, N, K, code), "w4a4_linear_w4a16")
+    return y
+
+
+def rotary_frequencies(axis_dims, theta=10000.0, device="cuda"):
+    """(freq [R/2] fp64, axis [R/2] int32) of qk_norm_rope for heads whose
+    first R = sum(axis_dims) elements rotate, axis_dims[a] of them with the
+    position on axis a: freq = theta^(-2 i / axis_dims[a]), i < axis_dims[a] / 2.
+    One axis for text, (height, width) for images, (time, height, width) for
+    video.  Made once and kept."""
+    dims = [int(d) for d in axis_dims]
+    if not dims or any(d < 2 or d % 2 for d in dims):
+        raise ValueError(f"axis_dims must be even numbers of at least 2, got {axis_dims}")
+    freq = [float(theta) ** (-2.0 * i / d) for d in dims for i in range(d // 2)]
+    axis = [a for a, d in enumerate(dims) for _ in range(d // 2)]
+    return (torch.tensor(freq, dtype=torch.float64, device=device),
+            torch.tensor(axis, dtype=torch.int32, device=device))
+
+
+def _heads(t, name, T, H, D, dtype, device):
+    """Strides (token, head) of a [T, H, D] tensor with contiguous D; a
+    dimension of one or no element has no stride of its own."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype} on {device}")
+    if t.dim() != 3 or t.shape != (T, H, D) or (t.stride(2) != 1 and t.numel()):
+        raise ValueError(f"{name} must be [{T}, {H}, {D}] with a contiguous last dimension, got {tuple(t.shape)}")
+    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, freq=None, axis=None, interleaved=True,
+                 eps=1e-6, q_out=None, k_out=None):
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (bf16 or fp16)
+    and their rotary rotation, in one pass -> (q, k) of the same shapes.
+      q_weight, k_weight [D]: weights of the norms; None leaves that norm out
+      positions [T, axes] (or [T]) int32 or int64; None leaves the rotation out
+      freq [R/2] fp64, axis [R/2] int32: of rotary_frequencies
+      interleaved: pairs (2i, 2i + 1), else (i, i + R/2)
+      k None: queries only; q_out / k_out may be q / k themselves."""
+    lib = _lib or load_library()
+    code = _need_16bit(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    dev, dtype = q.device, q.dtype
+    qt, qh = _heads(q, "q", T, Hq, D, dtype, dev)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+        qot, qoh = Hq * D, D
+    else:
+        qot, qoh = _heads(q_out, "q_out", T, Hq, D, dtype, dev)
+    Hk, kt, kh, kot, koh = 0, 0, 0, 0, 0
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k must be [T, Hk, D]")
+        Hk = k.shape[1]
+        kt, kh = _heads(k, "k", T, Hk, D, dtype, dev)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
+            kot, koh = Hk * D, D
+        else:
+            kot, koh = _heads(k_out, "k_out", T, Hk, D, dtype, dev)
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    if q_weight is not None:
+        _same(q_weight, dtype, (D,), "q_weight", dev)
+    if k_weight is not None:
+        _same(k_weight, dtype, (D,), "k_weight", dev)
+    bits, pt, axes, R = 0, 0, 0, 0
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.device != dev:
+            raise TypeError("positions must be a CUDA tensor on q's device")
+        if positions.dtype == torch.int32:
+            bits = 32
+        elif positions.dtype == torch.int64:
+            bits = 64
+        else:
+            raise TypeError(f"positions must be torch.int32 or torch.int64, got {positions.dtype}")
+        axes = positions.shape[1] if positions.dim() == 2 else 1
+        if positions.dim() not in (1, 2) or positions.shape[0] != T:
+            raise ValueError(f"positions must be [{T}, axes] or [{T}], got {tuple(positions.shape)}")
+        if positions.dim() == 2 and axes > 1 and positions.stride(1) != 1:
+            raise ValueError("positions must have a contiguous inner dimension")
+        pt = positions.stride(0) if T > 1 else axes
+        if freq is None or axis is None:
+            raise ValueError("positions need freq and axis (rotary_frequencies)")
+        R = 2 * freq.numel()
+        _same(freq, torch.float64, (R // 2,), "freq", dev)
+        _same(axis, torch.int32, (R // 2,), "axis", dev)
+    _call(lib.w4a4_qk_norm_rope, dev,
+          (q.data_ptr(), qt, qh, Hq, _addr(k), kt, kh, Hk, _addr(q_weight), _addr(k_weight), eps, _addr(positions),
+           bits, pt, axes, _addr(freq), _addr(axis), R, 1 if interleaved else 0, q_out.data_ptr(), qot, qoh,
+           _addr(k_out), kot, koh, T, D, code), "w4a4_qk_norm_rope")
+    return q_out, k_out
+
+
+def attention(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, causal=False, scale=None, out=None, return_lse=False):
+    """Softmax attention of q [Tq, Hq, D] over k, v [Tk, Hk, D] (bf16 or fp16,
+    D 64 or 128, Hq a multiple of Hk) -> out [Tq, Hq, D], or (out, lse [Tq, Hq]
+    fp32) with return_lse.
+      cu_seqlens_q, cu_seqlens_k [B + 1] int32 on the device: where each
+        packed sequence begins among the query and the key rows; both None:
+        one sequence
+      causal: query i of a sequence sees keys j <= i + Lk - Lq
+      scale: 1/sqrt(D) unless given
+    Rows behind the last sequence keep what `out` held (a new `out` holds
+    nothing defined there); queries that see no key get 0 and lse -inf."""
+    lib = _lib or load_library()
+    code = _need_16bit(q, "q")
+    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("q must be [Tq, Hq, D] and k, v [Tk, Hk, D]")
+    Tq, Hq, D = q.shape
+    Tk, Hk = k.shape[0], k.shape[1]
+    dev, dtype = q.device, q.dtype
+    qt, qh = _heads(q, "q", Tq, Hq, D, dtype, dev)
+    kt, kh = _heads(k, "k", Tk, Hk, D, dtype, dev)
+    vt, vh = _heads(v, "v", Tk, Hk, D, dtype, dev)
+    if out is None:
+        out = torch.empty((Tq, Hq, D), dtype=dtype, device=dev)
+        ot, oh = Hq * D, D
+    else:
+        ot, oh = _heads(out, "out", Tq, Hq, D, dtype, dev)
+    B = 1
+    if cu_seqlens_q is not None or cu_seqlens_k is not None:
+        if cu_seqlens_q is None or cu_seqlens_k is None:
+            raise ValueError("cu_seqlens_q and cu_seqlens_k go together")
+        B = cu_seqlens_q.numel() - 1
+        if B < 1:
+            raise ValueError("cu_seqlens_q must hold at least two numbers")
+        _same(cu_seqlens_q, torch.int32, (B + 1,), "cu_seqlens_q", dev)
+        _same(cu_seqlens_k, torch.int32, (B + 1,), "cu_seqlens_k", dev)
+    lse = torch.empty((Tq, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    # the workspace is the caller's own and lives in PyTorch's allocator (or a
+    # graph's pool) until the stream is past it, so overlapping calls and
+    # captured graphs never share one
+    nbytes = lib.w4a4_attention_workspace_bytes(Tq, Tk, B, Hq, Hk, D)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call(lib.w4a4_attention, dev,
+          (q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot, oh, _addr(lse),
+           _addr(cu_seqlens_q), _addr(cu_seqlens_k), B, Tq, Tk, Hq, Hk, D, 1 if causal else 0,
+           D ** -0.5 if scale is None else float(scale), code, _addr(ws), nbytes), "w4a4_attention")
+    return (out, lse) if return_lse else out
 
 
 def debug_set_wait_limit(limit_ns):
