@@ -387,7 +387,7 @@ int w4a4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  *       bad array reads and writes nothing out of range); both NULL with
  *       B == 1: one sequence of all the rows
  *   Rows of out and lse behind the last sequence keep what they hold.
- *   D in {64, 128}; Hq % Hk == 0; 1 <= Hq <= 65535; scale finite and > 0;
+ *   D in {64, 128}; Hq % Hk == 0; 1 <= Hq <= 65535; 0 < scale <= 1e38;
  *   0 <= Tq, Tk <= 2^30, B >= 1
  *   workspace: w4a4_attention_workspace_bytes(...) bytes of the same sizes
  *       (0 for most), 256-byte aligned, no initialisation needed.  Calls that

@@ -1,8 +1,50 @@
-// Softmax attention over packed sequences: full or causal, grouped heads.
+// Softmax attention over packed sequences: full or causal, grouped heads, long
+// prompts and single tokens.
+//
+//   s_j = scale q . k_j,  m = max_j s_j,  l = sum_j e^(s_j - m),
+//   out = sum_j e^(s_j - m) v_j / l,  lse = m + log l
+// in one pass over the keys: a running maximum and sum per row, the output
+// rescaled when the maximum moves.  4 D flops per (head, visible pair); on long
+// prompts the tensor cores and the exponentials bound it, over a cache for
+// few queries the bytes of k and v.
+//
+// Design (attention_tc_kernel<T, D, NQ, SPLIT>)
+//   * A CTA owns NQ tiles of 128 query rows of one key head and walks 128-key
+//     tiles.  The rows of a tile are (token, head) pairs: G heads that read
+//     the same key head times 128 / G tokens (one 3-D TMA box), so grouped
+//     heads share every key tile and a single token fills G rows of it.
+//   * Warp roles: one TMA producer warp (k and v tiles through one ring), one
+//     thread that issues the MMAs, and four softmax warps per query tile.
+//       S = Q K^T   tcgen05.mma kind::f16, 128 x 128 x D, both from shared memory
+//       O += P V    P from tensor memory, v as it lies (MN-major B operand)
+//     S (128 columns) and O (D columns) stay in tensor memory in fp32.
+//   * A softmax thread owns one row: it reads its 128 scores, so maximum and
+//     sum need no shuffles, and writes the weights, rounded to 16 bits (the
+//     MMA's operand type: half a step relative to each weight, in the sums of
+//     v only; the softmax's own sum takes them unrounded), over the scores.
+//   * With NQ = 2 the two tiles alternate: while the softmax of one runs, the
+//     tensor cores do O += P V and the next S of the other.  MMAs execute in
+//     issue order, so S(j + 1) may overwrite the P(j) that the MMA before it
+//     read, and a commit of S(j + 1) tells that O(j) is complete: the softmax
+//     warps rescale O themselves, no further role and no further barrier.
+//   * The maximum in use follows the running one only when it falls behind
+//     by more than 8 (in log2 units): weights stay below 2^8 and the rescaling
+//     of O, a round trip through tensor memory, becomes rare.  The result is
+//     the same quotient.
+//   * Masks select (-inf) rather than add, on the tiles they cut only.  Value
+//     rows behind a sequence's end inside its last tile are zeroed in
+//     shared memory, so whatever lies there reaches nothing.
+//   * Few rows (SPLIT): the keys of a sequence are cut into chunks, one CTA
+//     each (NQ = 1, two CTAs per SM); they write O and lse in fp32 to the
+//     workspace and attention_join_kernel weighs them by e^(lse_c - lse).
+//   Every wait is bounded; an expired wait records W4A4_ERR_TIMEOUT, every
+//   role stops, copies and MMAs drain and tensor memory is freed.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "half16.cuh"
 #include "ptx.cuh"
@@ -12,62 +54,602 @@
 namespace w4a4 {
 namespace {
 
+constexpr int kTile = 128;             // query rows per MMA tile and keys per key tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.f;        // how far (log2) the maximum in use may fall behind
+
 struct AttnArgs {
-  const uint16_t *q, *k, *v;
   uint16_t* out;
   float* lse;
-  int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;   // token and head strides in elements
+  int64_t o_t, o_h;                    // token and head strides in elements
   const int32_t *cu_q, *cu_k;
-  int B, Tq, Tk, Hq, Hk;
+  int B, Tq, Tk, Hq;
+  int G;                               // heads of one key head packed into a tile
+  int groups;                          // packed head sets per key head
+  int tokens;                          // tokens per 128-row tile: 128 / G
   int causal;
-  float scale;
+  float scale_log2;                    // scale * log2 e
+  int chunk;                           // SPLIT: key tiles per chunk
+  float* part_o;                       // SPLIT: [chunks][Tq][Hq][D]
+  float* part_lse;                     // SPLIT: [chunks][Tq][Hq], log2 units
+  unsigned int* status;
+  unsigned long long wait_ns;
 };
 
 __device__ __forceinline__ int cu_at(const int32_t* cu, int b, int total) {
   return cu == nullptr ? (b == 0 ? 0 : total) : min(max(cu[b], 0), total);
 }
 
-// One warp per query row and head; the running maximum and sum of the
-// softmax, one key at a time.
-template <class T, int D>
-__global__ void __launch_bounds__(256) attention_rows_kernel(const AttnArgs a) {
-  constexpr int E = D / 32;
+// Where a block works.
+struct Place {
+  int q0, nq;        // the sequence's first query row, their number
+  int k0, nk;        // the same of its keys
+  int tile;          // its number among the sequence's query tiles (NQ * tokens each)
+  int chunk;         // SPLIT: which chunk of the keys
+};
+
+// The place of block `index`: sequences in order, each with its query tiles
+// times its key chunks.  A warp walks the sequences 32 at a time.
+__device__ __forceinline__ bool find_place(const AttnArgs& a, int index, int tokens, int chunk_tiles, Place& p) {
   const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t row = w / a.Hq;
-  const int h = static_cast<int>(w - row * a.Hq);
-  if (row >= a.Tq) return;
-  // the sequence of this row: the last b with cu_q[b] <= row, if row < cu_q[b + 1]
-  int lo = 0, hi = a.B;
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    int q0 = 0, nq = 0, k0 = 0, nk = 0, n = 0, chunks = 1;
+    if (b < a.B) {
+      q0 = cu_at(a.cu_q, b, a.Tq);
+      nq = max(cu_at(a.cu_q, b + 1, a.Tq) - q0, 0);
+      k0 = cu_at(a.cu_k, b, a.Tk);
+      nk = max(cu_at(a.cu_k, b + 1, a.Tk) - k0, 0);
+      if (chunk_tiles != 0) chunks = max(1, ((nk + kTile - 1) / kTile + chunk_tiles - 1) / chunk_tiles);
+      n = (nq + tokens - 1) / tokens * chunks;
+    }
+    int incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > index);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      const int at = index - (before + __shfl_sync(0xFFFFFFFFu, incl - n, src));
+      const int ch = __shfl_sync(0xFFFFFFFFu, chunks, src);
+      p.q0 = __shfl_sync(0xFFFFFFFFu, q0, src);
+      p.nq = __shfl_sync(0xFFFFFFFFu, nq, src);
+      p.k0 = __shfl_sync(0xFFFFFFFFu, k0, src);
+      p.nk = __shfl_sync(0xFFFFFFFFu, nk, src);
+      p.tile = at / ch;
+      p.chunk = at - p.tile * ch;
+      return true;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  return false;
+}
+
+// The sequence that holds query row `row`.
+__device__ __forceinline__ bool find_token(const AttnArgs& a, int row, Place& p) {
+  int lo = 0, hi = a.B;                // the last sequence that begins at or before the row
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (cu_at(a.cu_q, mid, a.Tq) <= row) lo = mid; else hi = mid;
   }
-  const int q0 = cu_at(a.cu_q, lo, a.Tq), q1 = cu_at(a.cu_q, lo + 1, a.Tq);
-  if (row < q0 || row >= q1) return;
-  const int k0 = cu_at(a.cu_k, lo, a.Tk), k1 = cu_at(a.cu_k, lo + 1, a.Tk);
-  const int Lk = max(k1 - k0, 0);
-  int64_t seen = Lk;
-  if (a.causal) seen = min(static_cast<int64_t>(Lk), row - q0 + Lk - (q1 - q0) + 1);
-  const int hk = h / (a.Hq / a.Hk);
-  float qv[E], acc[E] = {};
-  for (int e = 0; e < E; ++e) qv[e] = T::to_f32(a.q[row * a.q_t + h * a.q_h + lane * E + e]);
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = 0; j < seen; ++j) {
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = fmaf(qv[e], T::to_f32(a.k[(k0 + j) * a.k_t + hk * a.k_h + lane * E + e]), s);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    s *= a.scale;
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : expf(m - mn);
-    const float p = s == -INFINITY ? 0.f : expf(s - mn);
-    l = l * f + p;
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, T::to_f32(a.v[(k0 + j) * a.v_t + hk * a.v_h + lane * E + e]), acc[e] * f);
-    m = mn;
+  p.q0 = cu_at(a.cu_q, lo, a.Tq);
+  p.nq = cu_at(a.cu_q, lo + 1, a.Tq) - p.q0;
+  p.k0 = cu_at(a.cu_k, lo, a.Tk);
+  p.nk = max(cu_at(a.cu_k, lo + 1, a.Tk) - p.k0, 0);
+  return row >= p.q0 && row < p.q0 + p.nq;
+}
+
+template <int D, int NQ>
+struct AttnShape {
+  static constexpr int kChunks = D / 64;                        // 64-column boxes of a row
+  static constexpr uint32_t kBox = kTile * 128;                 // 16 KB: 128 rows of 64 columns
+  static constexpr uint32_t kQBytes = NQ * kChunks * kBox;
+  static constexpr uint32_t kSlot = kChunks * kBox;             // one k or v tile
+  static constexpr int kSlots = NQ == 1 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 8);
+  static constexpr uint32_t kSmem = kQBytes + kSlots * kSlot + 1024;
+  static constexpr uint32_t kTmemCols = NQ == 1 ? 256 : 512;
+  static constexpr int kThreads = (NQ * 4 + 2) * 32;
+  static __device__ constexpr uint32_t s_col(int t) { return t * kTile; }
+  static __device__ constexpr uint32_t o_col(int t) { return NQ * kTile + t * D; }
+};
+
+template <int NQ, int SLOTS>
+struct AttnBars {
+  uint64_t q_full;
+  uint64_t full[SLOTS];
+  uint64_t empty[SLOTS];
+  uint64_t tail;           // the tile whose rows behind the sequence are zeroed
+  uint64_t s_full[NQ];     // scores of the next tile are in tensor memory
+  uint64_t p_full[NQ];     // weights are in tensor memory (and O is rescaled)
+  uint64_t o_full[NQ];     // the last O += P V is done
+  uint64_t drain;
+  Place place;
+  int found;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Wait by every lane of the warp; one verdict for all of them.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status,
+                                         unsigned long long wait_ns) {
+  const bool ok = mbar_wait(bar, parity, abort, status, wait_ns);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <class T, int D, int NQ, bool SPLIT>
+__global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+  using Shape = AttnShape<D, NQ>;
+  constexpr int kSlots = Shape::kSlots;
+  constexpr bool kBf16 = std::is_same<T, Bf16>::value;
+  extern __shared__ uint8_t smem_dyn[];
+  __shared__ AttnBars<NQ, kSlots> bars;
+  uint8_t* smem = align1024_shared(smem_dyn);
+  uint8_t* ring = smem + Shape::kQBytes;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  constexpr int kMmaWarp = NQ * 4;
+  constexpr int kLoadWarp = NQ * 4 + 1;
+
+  // q, k, v and the lengths may be the previous kernel's output (launched
+  // with programmatic stream serialization)
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      mbar_init(&bars.q_full, 1);
+      for (int s = 0; s < kSlots; ++s) {
+        mbar_init(&bars.full[s], 1);
+        mbar_init(&bars.empty[s], 1);
+      }
+      mbar_init(&bars.tail, 1);
+      for (int t = 0; t < NQ; ++t) {
+        mbar_init(&bars.s_full[t], 1);
+        mbar_init(&bars.p_full[t], 4);
+        mbar_init(&bars.o_full[t], 1);
+      }
+      mbar_init(&bars.drain, 1);
+      bars.abort_flag = 0;
+      fence_mbar_init();
+      fence_async_shared();
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    tmem_alloc(&bars.tmem_base, Shape::kTmemCols);
+    tmem_relinquish();
   }
-  const float r = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  for (int e = 0; e < E; ++e) a.out[row * a.o_t + h * a.o_h + lane * E + e] = T::from_f32(acc[e] * r);
-  if (a.lse != nullptr && lane == 0) a.lse[row * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+  griddep_wait();
+  if (warp == 0) {
+    // long causal tiles first: the block order runs backwards
+    const int index = a.causal ? static_cast<int>(gridDim.x - 1 - blockIdx.x) : static_cast<int>(blockIdx.x);
+    Place p{};
+    const bool found = find_place(a, index, NQ * a.tokens, SPLIT ? a.chunk : 0, p);
+    if (lane == 0) {
+      bars.place = p;
+      bars.found = found;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  const uint32_t tmem_base = bars.tmem_base;
+  const Place pl = bars.place;
+  volatile int* abort_flag = &bars.abort_flag;
+  if (bars.found) {
+    // key head, its first query head, and the tokens of the block
+    const int kh = static_cast<int>(blockIdx.y) / a.groups;
+    const int h0 = static_cast<int>(blockIdx.y) * a.G;
+    const int tok0 = pl.tile * NQ * a.tokens;
+    // key tiles [j0, n_t) of query tile t: up to the last key its last token sees
+    const int j0 = SPLIT ? pl.chunk * a.chunk : 0;
+    int n[NQ], n_all = 0;
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      const int first = tok0 + t * a.tokens;
+      const int last = min(first + a.tokens, pl.nq) - 1;
+      int seen = pl.nk;
+      if (a.causal) seen = min(seen, last + pl.nk - pl.nq + 1);
+      if (first >= pl.nq) seen = 0;
+      int end = (max(seen, 0) + kTile - 1) / kTile;
+      if (SPLIT) end = min(end, j0 + a.chunk);
+      n[t] = max(end - j0, 0);
+      n_all = max(n_all, n[t]);
+    }
+
+    if (warp == kLoadWarp) {
+      // ---------------------------------------------------------------- producer
+      if (n_all > 0) {
+        if (lane == 0) {
+          uint32_t boxes = 0;
+          for (int t = 0; t < NQ; ++t) boxes += n[t] > 0 ? 1 : 0;
+          const uint32_t rows = static_cast<uint32_t>(a.tokens * a.G);
+          mbar_arrive_expect_tx(&bars.q_full, boxes * Shape::kChunks * rows * 128);
+          for (int t = 0; t < NQ; ++t) {
+            if (n[t] == 0) continue;
+            for (int c = 0; c < Shape::kChunks; ++c)
+              tma_load_3d(smem + (t * Shape::kChunks + c) * Shape::kBox, &tmQ, &bars.q_full, 64 * c, h0,
+                          pl.q0 + tok0 + t * a.tokens);
+          }
+        }
+        int issued = 0;
+        bool tail_pending = false;
+        for (int i = 0; i < 2 * n_all; ++i) {
+          const int s = i % kSlots;
+          if (!wait_all(&bars.empty[s], ((i / kSlots) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) break;
+          const int row = (j0 + i / 2) * kTile;                 // first key of the tile, within the sequence
+          const bool is_v = (i & 1) != 0;
+          // value rows behind the sequence that are rows of the tensor (the
+          // copy itself zero-fills behind the tensor's end)
+          const bool cut = is_v && row + kTile > pl.nk && pl.k0 + pl.nk < a.Tk;
+          uint64_t* bar = cut ? &bars.tail : &bars.full[s];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, Shape::kSlot);
+            for (int c = 0; c < Shape::kChunks; ++c)
+              tma_load_3d(ring + s * Shape::kSlot + c * Shape::kBox, is_v ? &tmV : &tmK, bar, 64 * c, kh, pl.k0 + row);
+          }
+          __syncwarp();
+          ++issued;
+          if (cut) {   // at most once: the sequence's last tile
+            // the wait ignores the abort flag: the copy always lands
+            tail_pending = !wait_all(&bars.tail, 0, nullptr, a.status, a.wait_ns);
+            if (tail_pending) {
+              *abort_flag = 1;
+              break;
+            }
+            for (int c = 0; c < Shape::kChunks; ++c) {
+              const uint32_t base = smem_u32(ring + s * Shape::kSlot + c * Shape::kBox);
+              for (int e = (pl.nk - row) * 8 + lane; e < kTile * 8; e += 32) sts128(base + e * 16, make_uint4(0, 0, 0, 0));
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.full[s]);
+          }
+        }
+        // every issued copy lands before the CTA exits
+        if (lane == 0) {
+          (void)mbar_wait(&bars.q_full, 0, nullptr, nullptr, 100000000ull);
+          if (tail_pending) (void)mbar_wait(&bars.tail, 0, nullptr, nullptr, 100000000ull);
+          for (int s = 0; s < kSlots && s < issued; ++s) {
+            const int n_s = issued / kSlots + (s < issued % kSlots ? 1 : 0);
+            if (tail_pending && s == (issued - 1) % kSlots) continue;
+            (void)mbar_wait(&bars.full[s], static_cast<uint32_t>((n_s - 1) & 1), nullptr, nullptr, 100000000ull);
+          }
+        }
+        __syncwarp();
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0 && n_all > 0) {
+        constexpr uint32_t idesc_s = idesc_f16(kTile, kTile, kBf16, false);
+        constexpr uint32_t idesc_o = idesc_f16(kTile, D, kBf16, true);
+        const uint64_t qd = sw128_kmajor_desc(smem_u32(smem));
+        const uint64_t kd = sw128_kmajor_desc(smem_u32(ring));
+        const uint64_t vd = sw128_mnmajor_desc(smem_u32(ring), Shape::kBox);
+        auto score = [&](int t, int slot) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t step = (k / 4) * (Shape::kBox >> 4) + (k % 4) * 2;
+            mma_bf16(tmem_base + Shape::s_col(t), qd + t * (Shape::kChunks * Shape::kBox >> 4) + step,
+                     kd + slot * (Shape::kSlot >> 4) + step, idesc_s, k != 0 ? 1u : 0u);
+          }
+          mma_commit(&bars.s_full[t]);
+        };
+        bool ok = mbar_wait(&bars.q_full, 0, abort_flag, a.status, a.wait_ns) &&
+                  mbar_wait(&bars.full[0], 0, abort_flag, a.status, a.wait_ns);
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < NQ; ++t)
+            if (n[t] > 0) score(t, 0);
+          mma_commit(&bars.empty[0]);
+        }
+        for (int j = 0; ok && j < n_all; ++j) {
+          const int iv = 2 * j + 1, ik = 2 * j + 2;
+          const int sv = iv % kSlots, sk = ik % kSlots;
+          ok = mbar_wait(&bars.full[sv], (iv / kSlots) & 1, abort_flag, a.status, a.wait_ns);
+          bool k_ready = false;
+#pragma unroll
+          for (int t = 0; t < NQ; ++t) {
+            if (!ok || j >= n[t]) continue;
+            ok = mbar_wait(&bars.p_full[t], j & 1, abort_flag, a.status, a.wait_ns);
+            if (!ok) continue;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_f16_ts(tmem_base + Shape::o_col(t), tmem_base + Shape::s_col(t) + k * 8,
+                         vd + sv * (Shape::kSlot >> 4) + k * (16 * 128 >> 4), idesc_o, (j | k) != 0 ? 1u : 0u);
+            if (j + 1 == n[t]) mma_commit(&bars.o_full[t]);
+            // the last reader of this v tile frees its slot
+            if (t == NQ - 1 || j >= n[NQ - 1]) mma_commit(&bars.empty[sv]);
+            if (j + 1 < n[t]) {
+              if (!k_ready) {
+                ok = mbar_wait(&bars.full[sk], (ik / kSlots) & 1, abort_flag, a.status, a.wait_ns);
+                if (!ok) continue;
+                tc_fence_after();
+                k_ready = true;
+              }
+              score(t, sk);
+            }
+          }
+          if (ok && j + 1 < n_all) mma_commit(&bars.empty[sk]);
+        }
+        mma_commit(&bars.drain);
+        (void)mbar_wait(&bars.drain, 0, nullptr, nullptr, 100000000ull);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- softmax
+      const int t = warp >> 2;                       // query tile
+      const int r = (warp & 3) * 32 + lane;          // row of the tile = tensor-memory lane
+      const uint32_t lanes = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t s_at = lanes + Shape::s_col(t), o_at = lanes + Shape::o_col(t);
+      const int r_tok = r / a.G;
+      const int tok = tok0 + t * a.tokens + r_tok;   // within the sequence
+      const int head = h0 + r - r_tok * a.G;
+      const bool valid = r_tok < a.tokens && tok < pl.nq;
+      // keys this row sees, and the fewest any row of the tile sees, both counted from tile j0
+      int seen = pl.nk, fewest = pl.nk;
+      if (a.causal) {
+        seen = min(seen, tok + pl.nk - pl.nq + 1);
+        fewest = min(fewest, tok0 + t * a.tokens + pl.nk - pl.nq + 1);
+      }
+      seen -= j0 * kTile;
+      fewest -= j0 * kTile;
+      const int nt = n[t];
+      float m = -INFINITY;                           // the maximum in use, times scale_log2
+      uint64_t l2[2] = {0, 0};                       // partial sums (four fp32)
+      const float c = a.scale_log2;
+      bool ok = true;
+      for (int j = 0; j < nt; ++j) {
+        ok = wait_all(&bars.s_full[t], j & 1, abort_flag, a.status, a.wait_ns);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[4][32];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tmem_ld_32x32b_x32(s_at + 32 * g, sv[g]);
+        tmem_wait_ld();
+        if (fewest < (j + 1) * kTile) {              // a tile that a mask cuts (the same for the warp)
+          const int lim = seen - j * kTile;
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[g][i] = 32 * g + i < lim ? sv[g][i] : 0xFF800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          mx[g] = __uint_as_float(sv[g][0]);
+#pragma unroll
+          for (int i = 1; i < 31; i += 2) mx[g] = fmaxf(fmaxf(mx[g], __uint_as_float(sv[g][i])), __uint_as_float(sv[g][i + 1]));
+          mx[g] = fmaxf(mx[g], __uint_as_float(sv[g][31]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool behind = top - m > kRescale;      // false for -inf - -inf
+        if (j == 0) {
+          if (behind) m = top;
+        } else if (__any_sync(0xFFFFFFFFu, behind)) {
+          const float f = behind ? ex2(m - top) : 1.f;
+          if (behind) m = top;
+          const uint64_t ff = pack2(f, f);
+          const uint64_t zero = 0;
+          l2[0] = fma2(l2[0], ff, zero);
+          l2[1] = fma2(l2[1], ff, zero);
+#pragma unroll 1
+          for (int g = 0; g < D / 16; ++g) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(o_at + 16 * g, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_32x32b_x16(o_at + 16 * g, o);
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : -m;
+        const uint64_t cc = pack2(c, c), ss = pack2(shift, shift);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            uint32_t* e = &sv[g][2 * i];
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(e[0]), __uint_as_float(e[1])), cc, ss));
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            e[0] = __float_as_uint(p0);
+            e[1] = __float_as_uint(p1);
+            p[i] = T::from_f32x2(p0, p1);
+          }
+          tmem_st_32x32b_x16(s_at + 16 * g, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[t]);
+        // the sum, off the path of the MMA
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const uint32_t* e = &sv[i / 16][(2 * i) % 32];
+          l2[0] = add2(l2[0], pack2(__uint_as_float(e[0]), __uint_as_float(e[1])));
+          l2[1] = add2(l2[1], pack2(__uint_as_float(e[2]), __uint_as_float(e[3])));
+        }
+      }
+      if (ok && nt > 0) {
+        ok = wait_all(&bars.o_full[t], 0, abort_flag, a.status, a.wait_ns);
+        tc_fence_after();
+      }
+      if (ok) {
+        // ---- out = O / l, lse = m + log l (log2 units until the end)
+        const float2 la = unpack2(add2(l2[0], l2[1]));
+        const float l = la.x + la.y;
+        const float inv = l == 0.f ? 0.f : 1.f / l;            // no key seen: 0 (l is NaN for NaN scores)
+        const float lse2 = l == 0.f ? -INFINITY : m + lg2(l);
+        const int64_t row = static_cast<int64_t>(pl.q0) + tok;
+        float* po = nullptr;
+        uint16_t* out = nullptr;
+        if (valid) {
+          const int64_t at = row * a.Hq + head;
+          if (SPLIT) {
+            const int64_t pat = static_cast<int64_t>(pl.chunk) * a.Tq * a.Hq + at;
+            a.part_lse[pat] = lse2;
+            po = a.part_o + pat * D;
+          } else {
+            if (a.lse != nullptr) a.lse[at] = lse2 * kLn2;
+            out = a.out + row * a.o_t + head * a.o_h;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < D / 32; ++g) {
+          uint32_t o[32];
+          if (nt > 0) {                              // the same for the warp
+            tmem_ld_32x32b_x32(o_at + 32 * g, o);
+            tmem_wait_ld();
+          }
+          if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(nt > 0 && l != 0.f ? __uint_as_float(o[i]) * inv : 0.f);
+            if (SPLIT) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(po + 32 * g + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = T::from_f32x2(__uint_as_float(o[i + 2 * e]), __uint_as_float(o[i + 2 * e + 1]));
+                *reinterpret_cast<uint4*>(out + 32 * g + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+          __syncwarp();                              // the loads are collective
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Shape::kTmemCols);
+  }
+}
+
+// out = sum_c e^(lse_c - lse) O_c over the chunks of a row's keys, lse = log
+// sum_c e^(lse_c); one warp per (token, head), chunks in order.
+template <class T, int D>
+__global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
+  constexpr int E = D / 32;
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t rows = static_cast<int64_t>(a.Tq) * a.Hq;
+  if (w >= rows) return;
+  const int tok = static_cast<int>(w / a.Hq);
+  const int head = static_cast<int>(w - static_cast<int64_t>(tok) * a.Hq);
+  Place p{};
+  if (!find_token(a, tok, p)) return;
+  const int tiles = (p.nk + kTile - 1) / kTile;
+  const int chunks = max(1, (tiles + a.chunk - 1) / a.chunk);
+  float top = -INFINITY;
+  for (int c = lane; c < chunks; c += 32) top = fmaxf(top, a.part_lse[c * rows + w]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[E] = {};
+#pragma unroll 4
+  for (int c = 0; c < chunks; ++c) {
+    const float z = a.part_lse[c * rows + w];
+    if (z == -INFINITY) continue;                    // a chunk of which nothing is seen
+    const float f = ex2(z - base);
+    sum += f;
+    const float* o = a.part_o + (c * rows + w) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, o[e], acc[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t* out = reinterpret_cast<uint32_t*>(a.out + tok * a.o_t + head * a.o_h + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[e / 2] = T::from_f32x2(acc[e] * inv, acc[e + 1] * inv);
+  if (a.lse != nullptr && lane == 0) a.lse[w] = sum == 0.f ? -INFINITY : (base + lg2(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------ host side
+// How a call is cut into blocks.  A function of the sizes alone, so that the
+// workspace size is one too (148 SMs: a B200).
+struct Plan {
+  int G, tokens, nq;
+  int chunk;            // key tiles per chunk, 0: not split
+  int64_t blocks;       // upper bound of (query tile, chunk) pairs over the sequences
+  int64_t chunks;       // upper bound of chunks of one sequence
+};
+
+Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
+  Plan p{};
+  const int64_t share = Hq / Hk;
+  // heads per tile: the largest divisor of the group that leaves at most 8 of
+  // the tile's 128 rows empty
+  p.G = 1;
+  for (int d = 1; d <= kTile && d <= share; ++d)
+    if (share % d == 0 && kTile / d * d >= 120) p.G = d;
+  p.tokens = kTile / p.G;
+  const int64_t sets = Hq / p.G;
+  const int64_t two = (Tq / (2 * p.tokens) + B) * sets;
+  const int64_t one = (Tq / p.tokens + B) * sets;
+  p.nq = Tq <= B * p.tokens || two < 148 ? 1 : 2;
+  p.blocks = p.nq == 1 ? Tq / p.tokens + B : Tq / (2 * p.tokens) + B;
+  p.chunks = 1;
+  if (p.nq == 1 && one < 296) {
+    // about three rounds of two blocks per SM, chunks of four key tiles at least
+    const int64_t tiles = (Tk + kTile - 1) / kTile;
+    int64_t chunk = (tiles * one + B * 888 - 1) / (B * 888);
+    if (chunk < 4) chunk = 4;
+    if (chunk * B < tiles) {
+      p.chunk = static_cast<int>(chunk);
+      const int64_t most = (Tq + p.tokens - 1) / p.tokens;      // query tiles of one sequence
+      const int64_t x = most * (tiles / chunk + B), y = (Tq / p.tokens + B) * (tiles / chunk + 1);
+      p.blocks = x < y ? x : y;
+      p.chunks = (tiles + chunk - 1) / chunk;
+    }
+  }
+  return p;
 }
 
 int check_heads(const void* p, int64_t t, int64_t h, int64_t T, int64_t H, int64_t D) {
@@ -78,6 +660,62 @@ int check_heads(const void* p, int64_t t, int64_t h, int64_t T, int64_t H, int64
   return W4A4_OK;
 }
 
+
+// 3-D map over a [tokens, heads, D] tensor of 16-bit elements (strides in
+// elements): box {64, box_heads, box_tokens}, 128-byte swizzle; rows out of
+// range read as zero.
+int heads_map(CUtensorMap* map, const void* base, bool bf16, int64_t T, int64_t H, int64_t D, int64_t t_stride,
+              int64_t h_stride, int box_heads, int box_tokens) {
+  return tensor_map_3d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, D, H, T,
+                       2 * (H > 1 ? h_stride : D), 2 * (T > 1 ? t_stride : H * D), 64, box_heads, box_tokens,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <class T, int D, int NQ, bool SPLIT>
+cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnArgs& a,
+                      int64_t blocks, int64_t sets, cudaStream_t stream) {
+  using Shape = AttnShape<D, NQ>;
+  auto kernel = attention_tc_kernel<T, D, NQ, SPLIT>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(sets), 1);
+  cfg.blockDim = dim3(Shape::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Shape::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, tmQ, tmK, tmV, a);
+  if (e != cudaSuccess || !SPLIT) return e;
+  const int64_t rows = static_cast<int64_t>(a.Tq) * a.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4), 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D>, a);
+}
+
+template <class T, int D>
+cudaError_t launch_plan(const Plan& p, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                        const AttnArgs& a, cudaStream_t stream) {
+  const int64_t sets = a.Hq / p.G;
+  if (p.chunk != 0) return launch_tc<T, D, 1, true>(tmQ, tmK, tmV, a, p.blocks, sets, stream);
+  if (p.nq == 1) return launch_tc<T, D, 1, false>(tmQ, tmK, tmV, a, p.blocks, sets, stream);
+  return launch_tc<T, D, 2, false>(tmQ, tmK, tmV, a, p.blocks, sets, stream);
+}
+
 }  // namespace
 }  // namespace w4a4
 
@@ -85,7 +723,13 @@ using namespace w4a4;
 
 extern "C" {
 
-size_t w4a4_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+// SPLIT: [chunks][Tq][Hq][D] fp32 partial outputs, [chunks][Tq][Hq] fp32 lse
+size_t w4a4_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
+  if (Tq <= 0 || Tk < 0 || B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || D < 1) return 0;
+  const Plan p = make_plan(Tq, Tk, B, Hq, Hk);
+  if (p.chunk == 0) return 0;
+  return static_cast<size_t>(p.chunks) * static_cast<size_t>(Tq) * static_cast<size_t>(Hq) * (D + 1) * 4;
+}
 
 int w4a4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
                    int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
@@ -101,7 +745,7 @@ int w4a4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
   if (D != 64 && D != 128) return W4A4_ERR_SHAPE;
   if (Hq < 1 || Hq > 65535 || Hk < 1 || Hq % Hk != 0) return W4A4_ERR_SHAPE;
   if (dtype != W4A4_BF16 && dtype != W4A4_FP16) return W4A4_ERR_ARG;
-  if (!(scale > 0.f) || scale > 3.0e38f) return W4A4_ERR_ARG;
+  if (!(scale > 0.f) || scale > 1.0e38f) return W4A4_ERR_ARG;
   int st;
   if ((st = check_heads(q, q_token_stride, q_head_stride, Tq, Hq, D)) != W4A4_OK) return st;
   if ((st = check_heads(out, out_token_stride, out_head_stride, Tq, Hq, D)) != W4A4_OK) return st;
@@ -114,27 +758,38 @@ int w4a4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
   const size_t need = w4a4_attention_workspace_bytes(Tq, Tk, B, Hq, Hk, D);
   if (need != 0 && (workspace == nullptr || workspace_bytes < need || !aligned_to(workspace, 256)))
     return W4A4_ERR_WORKSPACE;
+  const Plan p = make_plan(Tq, Tk, B, Hq, Hk);
+  if (p.blocks > 0x7FFFFFFF) return W4A4_ERR_SHAPE;
   AttnArgs a{};
-  a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  a.q_t = q_token_stride, a.q_h = q_head_stride;
-  a.k_t = k_token_stride, a.k_h = k_head_stride;
-  a.v_t = v_token_stride, a.v_h = v_head_stride;
   a.o_t = out_token_stride, a.o_h = out_head_stride;
   a.cu_q = cu_q, a.cu_k = cu_k;
-  a.B = static_cast<int>(B), a.Tq = static_cast<int>(Tq), a.Tk = static_cast<int>(Tk);
-  a.Hq = static_cast<int>(Hq), a.Hk = static_cast<int>(Hk);
+  a.B = static_cast<int>(B), a.Tq = static_cast<int>(Tq), a.Tk = static_cast<int>(Tk), a.Hq = static_cast<int>(Hq);
+  a.G = p.G;
+  a.groups = static_cast<int>(Hq / Hk) / p.G;
+  a.tokens = p.tokens;
   a.causal = causal != 0;
-  a.scale = scale;
-  const int64_t blocks = (Tq * Hq + 7) / 8;
-  auto kernel = dtype == W4A4_BF16 ? (D == 64 ? attention_rows_kernel<Bf16, 64> : attention_rows_kernel<Bf16, 128>)
-                                   : (D == 64 ? attention_rows_kernel<Fp16, 64> : attention_rows_kernel<Fp16, 128>);
-  if (blocks > 0x7FFFFFFF) return W4A4_ERR_SHAPE;
-  kernel<<<static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? W4A4_OK : W4A4_ERR_CUDA;
+  a.scale_log2 = scale * kLog2e;
+  a.chunk = p.chunk;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = a.part_o + (p.chunk != 0 ? p.chunks * Tq * Hq * D : 0);
+  a.status = dev->status;
+  a.wait_ns = wait_limit_ns();
+  const bool bf16 = dtype == W4A4_BF16;
+  CUtensorMap tmQ, tmK, tmV;
+  if ((st = heads_map(&tmQ, q, bf16, Tq, Hq, D, q_token_stride, q_head_stride, p.G, p.tokens)) != W4A4_OK) return st;
+  if (Tk == 0) {
+    tmK = tmV = tmQ;     // never read: no key tile
+  } else {
+    if ((st = heads_map(&tmK, k, bf16, Tk, Hk, D, k_token_stride, k_head_stride, 1, kTile)) != W4A4_OK) return st;
+    if ((st = heads_map(&tmV, v, bf16, Tk, Hk, D, v_token_stride, v_head_stride, 1, kTile)) != W4A4_OK) return st;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (bf16) e = D == 64 ? launch_plan<Bf16, 64>(p, tmQ, tmK, tmV, a, s) : launch_plan<Bf16, 128>(p, tmQ, tmK, tmV, a, s);
+  else e = D == 64 ? launch_plan<Fp16, 64>(p, tmQ, tmK, tmV, a, s) : launch_plan<Fp16, 128>(p, tmQ, tmK, tmV, a, s);
+  return e == cudaSuccess ? W4A4_OK : W4A4_ERR_CUDA;
 }
 
 }  // extern "C"

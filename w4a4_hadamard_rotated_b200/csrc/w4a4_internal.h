@@ -141,6 +141,12 @@ cudaError_t lora_up_launch(const uint16_t* t, const uint16_t* B, uint16_t* y, in
 int tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, int64_t rows, int64_t cols,
                   int64_t row_stride_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle);
 
+// Generic 3-D TMA map: extents {d0, d1, d2} (d0 innermost, contiguous), strides of d1
+// and d2 in bytes, box {box0, box1, box2}; out-of-range elements read as zero.
+int tensor_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, int64_t d0, int64_t d1, int64_t d2,
+                  int64_t stride1_bytes, int64_t stride2_bytes, int box0, int box1, int box2,
+                  CUtensorMapSwizzle swizzle);
+
 // ---- tiny-M weight streaming on the CUDA cores (gemv.cu)
 struct GemvArgs {
   const int8_t* xq;       // [M, K/2]
