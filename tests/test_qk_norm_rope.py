@@ -179,6 +179,19 @@ def test_values_at_the_edges(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("inter", [True, False])
+def test_what_does_not_turn_keeps_its_bits(cuda_lib, inter):
+    """Without norms, elements past R are copied: negative zeros, NaN and
+    infinities next to them included."""
+    q, _, _, _ = make(4, 3, 1, 64, torch.bfloat16)
+    q[:, :, 40], q[:, :, 43], q[:, :, 63] = -0.0, float("nan"), float("inf")
+    freq, axis = w4.rotary_frequencies((32,))
+    out, _ = w4.qk_norm_rope(q, None, None, None, places(4, 1, 9), freq, axis, interleaved=inter)
+    assert torch.equal(out[:, :, 32:].contiguous().view(torch.int16), q[:, :, 32:].contiguous().view(torch.int16))
+    check(out[:, :, :32], reference(q[:, :, :32], None, 0, places(4, 1, 9), freq, axis, inter))
+
+
+@pytest.mark.gpu
 def test_empty_graph_and_stream(cuda_lib):
     q, k, qw, kw = make(19, 8, 4, 128, torch.bfloat16)
     freq, axis = w4.rotary_frequencies((64, 64))
