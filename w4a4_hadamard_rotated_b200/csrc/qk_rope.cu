@@ -14,12 +14,17 @@
 //   * The angles depend on the token only.  A block takes a few whole tokens:
 //     its threads form each token's R/2 sines and cosines once into shared
 //     memory, every warp then keeps those of its elements in registers for
-//     all heads of its token, the norm's weights too.
+//     all heads of its token, multiplied with the norm's weights: an element
+//     is r (own u_i + other u_pair), r the reciprocal root of its head.
 //   * The angle is reduced in turns: position * freq / 2 pi in fp64, less its
 //     nearest whole number, then sincospi in fp32.  In fp32 a position of
-//     2^17 would leave 7 bits of the fraction of a turn.
-//   * Four loads of a warp are in flight before the first is used, the first
-//     four while the angles are formed.
+//     2^17 leaves 10 bits of the fraction of a turn.
+//   * Four to eight loads of a lane are in flight before the first is used, the
+//     first of a token while its angles are formed.  The blocks stay: each walks
+//     over tokens, so a token's latency hides behind the other warps' streams
+//     (blocks of one token each took 427 us where these take 219).
+// Measured: 32760 tokens, 40 + 40 heads of 128: 219 us, 6.1 TB/s; 4608 tokens,
+// 24 + 24 heads: 25 us; one token of 32 + 8 heads 4.4 us, all of it latency.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -60,7 +65,13 @@ struct RopeArgs {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeBatch = 4;          // heads (times 32 / LPH) a warp has in flight
+// Blocks per SM and 16-byte loads a lane has in flight: three of 80 registers
+// and four loads where that fits without spilling, else two and eight.
+// Measured at 32760 tokens of 40 + 40 heads of 128 (1.34 GB): interleaved 219 us
+// against 223, halves (which need the pair's angles and weights too) 247 against
+// 246 with spills; at 1001 tokens of 32 + 8 heads of 64, halves 6.2 against 7.8 us.
+constexpr int rope_blocks(bool inter, bool copy) { return inter && !copy ? 3 : 2; }
+constexpr int rope_batch(bool inter, bool copy) { return inter && !copy ? 4 : 8; }
 
 __device__ __forceinline__ uint4 ldg128(const uint16_t* p) {
   uint4 v;
@@ -71,157 +82,256 @@ __device__ __forceinline__ uint4 ldg128(const uint16_t* p) {
   return v;
 }
 
-// warps_per_token: 1, 2, 4 or 8; a block takes 8 / warps_per_token tokens.
-template <class T, int LPH, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_kernel(const RopeArgs a, const int warps_per_token) {
-  constexpr int kHeads = 32 / LPH;     // heads per warp and step
-  constexpr int kAngles = INTER ? 4 : 8;
-  __shared__ __align__(16) float cs[kRopeWarps][kRopeMaxD / 2], sn[kRopeWarps][kRopeMaxD / 2];
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// One side (queries or keys) of one token: this lane's elements of the heads
+// first, first + step, ...
+// COPY: some elements do not turn (R < D).
+template <class T, int LPH, bool INTER, bool COPY>
+struct RopeWalk {
+  static constexpr int kBatch = rope_batch(INTER, COPY);
+  const uint16_t* in;
+  uint16_t* out;
+  int64_t in_step, out_step;
+  int left;                                          // heads from this lane's first one on
+  int step;
+  bool active;                                       // the lane holds elements of its token's heads
+  uint4 x[kBatch];
+
+  __device__ __forceinline__ void init(const RopeSide& side, int H, int64_t t, int e, int head, int step_, bool active_) {
+    in = side.in + t * side.in_t + head * side.in_h + 8 * e;
+    out = side.out + t * side.out_t + head * side.out_h + 8 * e;
+    in_step = step_ * side.in_h;
+    out_step = step_ * side.out_h;
+    left = H - head;
+    step = step_;
+    active = active_;
+  }
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      x[b] = make_uint4(0u, 0u, 0u, 0u);
+      if (active && b * step < left) x[b] = ldg128(in + b * in_step);
+    }
+    in += kBatch * in_step;
+  }
+  // own[i], other[i]: what this element and its pair's other one contribute
+  // to element i, the weights of the norm included.  `from`: halves: the lane
+  // of the pair's other element.  `copy`: bit i: word i is copied.
+  __device__ __forceinline__ void run(bool norm, float inv_d, float eps, const float (&own)[8], const float (&other)[8],
+                                      int from, uint32_t copy, int steps) {
+    for (; steps > 0; steps -= kBatch) {         // the same for the warp
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (b >= steps) break;
+        const uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = T::to_f32x2(w[i]);
+          u[2 * i] = f.x;
+          u[2 * i + 1] = f.y;
+        }
+        float r = 1.f;
+        if (norm) {
+          float sum = u[0] * u[0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) sum = fmaf(u[i], u[i], sum);
+#pragma unroll
+          for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+          r = rsqrtf(fmaf(sum, inv_d, eps));
+        }
+        float v[8];
+        if (INTER) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = fmaf(u[i ^ 1], other[i], u[i] * own[i]) * r;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = T::to_f32x2(__shfl_sync(0xFFFFFFFFu, w[i], from));
+            v[2 * i] = fmaf(f.x, other[2 * i], u[2 * i] * own[2 * i]) * r;
+            v[2 * i + 1] = fmaf(f.y, other[2 * i + 1], u[2 * i + 1] * own[2 * i + 1]) * r;
+          }
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = T::from_f32x2(v[2 * i], v[2 * i + 1]);
+        if (COPY) {
+          // what does not turn: the element times its weight, or its bits where
+          // there is no norm (NaN and infinities next to it included)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (copy >> i & 1)
+              o[i] = norm ? T::from_f32x2(u[2 * i] * own[2 * i] * r, u[2 * i + 1] * own[2 * i + 1] * r) : w[i];
+        }
+        if (active && b * step < left) *reinterpret_cast<uint4*>(out + b * out_step) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      out += kBatch * out_step;
+      left -= kBatch * step;
+      if (steps > kBatch) load();
+    }
+  }
+};
+
+// 16 bytes of shared memory as floats.
+__device__ __forceinline__ void lds4(const float* p, float* v) {
+  const float4 f = *reinterpret_cast<const float4*>(p);
+  v[0] = f.x;
+  v[1] = f.y;
+  v[2] = f.z;
+  v[3] = f.w;
+}
+
+// `parts` warps (1, 2, 4 or 8, of one block) share a token.
+template <class T, int LPH, bool INTER, bool COPY>
+__global__ void __launch_bounds__(kRopeThreads, rope_blocks(INTER, COPY)) qk_norm_rope_kernel(const RopeArgs a, const int parts) {
+  constexpr int kHeads = 32 / LPH;                   // heads per warp and step
+  __shared__ double freq[kRopeMaxD / 2];
+  __shared__ int axis[kRopeMaxD / 2];
+  __shared__ __align__(16) float weights[2][kRopeMaxD];   // of the norms of q and k; 1 without
+  // per token: cosines and sines, from the angle's half = R / 2 on those of no turn
+  __shared__ __align__(16) float cs[kRopeWarps][kRopeMaxD / 2 + 8], sn[kRopeWarps][kRopeMaxD / 2 + 8];
   // q, k, the weights and the positions may be the previous kernel's output
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tokens = kRopeWarps / warps_per_token;
-  const int slot = warp / warps_per_token;           // which token of the block
-  const int part = warp - slot * warps_per_token;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
-  const int64_t t = t0 + slot;
+  const int tokens = kRopeWarps / parts;
+  const int slot = warp / parts, part = warp - slot * parts;
   const int e = lane & (LPH - 1);                    // elements 8 e .. 8 e + 7 of the head
-  const bool active = t < a.T && 8 * e < a.D;
-  const int step = warps_per_token * kHeads;
-  const int first = part * kHeads + lane / LPH;
+  const bool active = 8 * e < a.D;
+  const int step = parts * kHeads;
+  const int half = a.R >> 1;
+  const int head = part * kHeads + lane / LPH;
 
-  const uint16_t* qi = a.q.in + t * a.q.in_t + 8 * e;
-  const uint16_t* ki = a.k.in + t * a.k.in_t + 8 * e;
-  uint16_t* qo = a.q.out + t * a.q.out_t + 8 * e;
-  uint16_t* ko = a.k.out + t * a.k.out_t + 8 * e;
-  uint4 next[kRopeBatch];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int b = 0; b < kRopeBatch; ++b) {
-      const int h = h0 + b * step;
-      if (active && h < a.H)
-        next[b] = ldg128(h < a.Hq ? qi + h * a.q.in_h : ki + (h - a.Hq) * a.k.in_h);
-      else
-        next[b] = make_uint4(0u, 0u, 0u, 0u);
+  RopeWalk<T, LPH, INTER, COPY> walk;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * tokens + slot;
+  double pos = 0.;                                   // lane i: the position on axis i
+  auto begin = [&] {
+    walk.init(a.q, a.Hq, t, e, head, step, active);
+    walk.load();
+    if (lane < a.axes && half != 0) {
+      const int64_t at = t * a.pos_stride + lane;
+      pos = a.pos64 ? static_cast<double>(static_cast<const int64_t*>(a.positions)[at])
+                    : static_cast<double>(static_cast<const int32_t*>(a.positions)[at]);
     }
   };
-  load(first);
-
-  const int half = a.R >> 1;
-  for (int i = threadIdx.x; i < tokens * half; i += kRopeThreads) {
-    const int s = i / half, j = i - s * half;
-    if (t0 + s >= a.T) break;
-    const int ax = min(max(a.axis[j], 0), a.axes - 1);
-    const int64_t at = (t0 + s) * a.pos_stride + ax;
-    const double pos = a.pos64 ? static_cast<double>(static_cast<const int64_t*>(a.positions)[at])
-                               : static_cast<double>(static_cast<const int32_t*>(a.positions)[at]);
-    double turns = pos * (a.freq[j] * 0.15915494309189533577);   // 1 / (2 pi)
-    turns -= rint(turns);
-    float sv, cv;
-    sincospif(2.f * static_cast<float>(turns), &sv, &cv);
-    cs[s][j] = cv;
-    sn[s][j] = sv;
+  if (t < a.T) begin();
+  for (int j = threadIdx.x; j < half; j += kRopeThreads) {
+    freq[j] = a.freq[j] * 0.15915494309189533577;    // in turns: 1 / (2 pi)
+    axis[j] = min(max(a.axis[j], 0), a.axes - 1);
+  }
+  for (int j = threadIdx.x; j < 2 * kRopeMaxD; j += kRopeThreads) {
+    const uint16_t* w = j < kRopeMaxD ? a.q.weight : a.k.weight;
+    const int d = j & (kRopeMaxD - 1);
+    weights[j / kRopeMaxD][d] = w != nullptr && d < a.D ? T::to_f32(w[d]) : 1.f;
+  }
+  for (int j = half + lane; j < kRopeMaxD / 2 + 8; j += 32) {
+    cs[warp][j] = 1.f;
+    sn[warp][j] = 0.f;
   }
   __syncthreads();
 
-  // this lane's angles (0 turns where nothing rotates) and weights
-  float c[kAngles], s[kAngles];
-  int from = lane;                                   // halves: the partner's lane
-  {
-    int at = -1;
-    float sign = 1.f;
-    if (INTER) {
-      if (8 * e < a.R) at = 4 * e;
-    } else if (8 * e < a.R) {
+  int from = lane;                                   // halves: the lane of the pair's other element
+  int angle = 4 * e;                                 // the lane's first angle
+  int pair = 8 * e;                                  // halves: the pair's other element of the lane's first one
+  float sign = 1.f;
+  if (!INTER) {
+    angle = kRopeMaxD / 2;                           // no turn
+    if (8 * e < a.R) {
       const bool low = 8 * e < half;
-      at = low ? 8 * e : 8 * e - half;
+      angle = low ? 8 * e : 8 * e - half;
+      pair = low ? 8 * e + half : 8 * e - half;
       from = low ? lane + half / 8 : lane - half / 8;
-      sign = low ? -1.f : 1.f;                       // a cos - b sin, b cos + a sin
-    }
-#pragma unroll
-    for (int i = 0; i < kAngles; ++i) {
-      const bool turned = at >= 0 && at + i < half;
-      c[i] = turned ? cs[slot][at + i] : 1.f;
-      s[i] = turned ? (INTER ? sn[slot][at + i] : sign * sn[slot][at + i]) : 0.f;
+      sign = low ? -1.f : 1.f;
     }
   }
-  const uint32_t one = T::from_f32x2(1.f, 1.f);
-  uint4 wq = make_uint4(one, one, one, one), wk = wq;
-  const bool norm_q = a.q.weight != nullptr, norm_k = a.k.weight != nullptr;
-  if (norm_q && 8 * e < a.D) wq = *reinterpret_cast<const uint4*>(a.q.weight + 8 * e);
-  if (norm_k && 8 * e < a.D) wk = *reinterpret_cast<const uint4*>(a.k.weight + 8 * e);
+  uint32_t copy = 0;                                 // words that do not turn
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (8 * e + 2 * i >= a.R) copy |= 1u << i;
   const float inv_d = 1.f / static_cast<float>(a.D);
 
-  for (int h0 = part * kHeads; h0 < a.H; h0 += kRopeBatch * step) {   // the same for the warp
-    const int mine = h0 + lane / LPH;
-#pragma unroll
-    for (int b = 0; b < kRopeBatch; ++b) {
-      const int h = mine + b * step;
-      const bool is_q = h < a.Hq;
-      const uint32_t w[4] = {is_q ? wq.x : wk.x, is_q ? wq.y : wk.y, is_q ? wq.z : wk.z, is_q ? wq.w : wk.w};
-      const uint32_t in[4] = {next[b].x, next[b].y, next[b].z, next[b].w};
-      float u[8];
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = T::to_f32x2(in[i]);
-        u[2 * i] = f.x;
-        u[2 * i + 1] = f.y;
-        sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
+  while (t < a.T) {                                  // the same for the warps of a token
+    for (int j0 = part * 32; j0 < half; j0 += parts * 32) {
+      const int j = min(j0 + lane, half - 1);
+      double turns = __shfl_sync(0xFFFFFFFFu, pos, axis[j]) * freq[j];
+      turns -= rint(turns);
+      float sv, cv;
+      sincospif(2.f * static_cast<float>(turns), &sv, &cv);
+      if (j0 + lane < half) {
+        cs[slot][j] = cv;
+        sn[slot][j] = sv;
       }
-#pragma unroll
-      for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-      const bool norm = is_q ? norm_q : norm_k;
-      const float r = norm ? rsqrtf(fmaf(sum, inv_d, a.eps)) : 1.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 g = T::to_f32x2(w[i]);
-        u[2 * i] *= r * g.x;
-        u[2 * i + 1] *= r * g.y;
+    }
+    bar_sync(1 + slot, parts * 32);
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const bool norm = (side == 0 ? a.q.weight : a.k.weight) != nullptr;
+      const int H = side == 0 ? a.Hq : a.H - a.Hq;
+      if (side == 1) {
+        if (H == 0) break;
+        walk.init(a.k, H, t, e, head, step, active);
+        walk.load();
       }
-      uint32_t out[4];
+      // element i turns into own * u_i + other * u_pair
+      float own[8], other[8], w[8];
+      lds4(&weights[side][8 * e], w);
+      lds4(&weights[side][8 * e + 4], w + 4);
       if (INTER) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool turned = 8 * e + 2 * i < a.R;
-          const float x = u[2 * i] * c[i % kAngles] - u[2 * i + 1] * s[i % kAngles];
-          const float y = u[2 * i] * s[i % kAngles] + u[2 * i + 1] * c[i % kAngles];
-          out[i] = T::from_f32x2(turned ? x : u[2 * i], turned ? y : u[2 * i + 1]);
-          if (!turned && !norm) out[i] = in[i];       // copied bit for bit, NaN included
-        }
-      } else {
-        float v[8];
+        float c[4], s[4];
+        lds4(&cs[slot][angle], c);
+        lds4(&sn[slot][angle], s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float other = __shfl_sync(0xFFFFFFFFu, u[i], from);
-          v[i] = from == lane ? u[i] : fmaf(u[i], c[i % kAngles], other * s[i % kAngles]);
+          own[i] = c[i / 2] * w[i];
+          other[i] = (i & 1 ? s[i / 2] : -s[i / 2]) * w[i ^ 1];
         }
+      } else {
+        float c[8], s[8], wp[8];
+        lds4(&cs[slot][angle], c);
+        lds4(&cs[slot][angle + 4], c + 4);
+        lds4(&sn[slot][angle], s);
+        lds4(&sn[slot][angle + 4], s + 4);
+        lds4(&weights[side][pair], wp);
+        lds4(&weights[side][pair + 4], wp + 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          out[i] = T::from_f32x2(v[2 * i], v[2 * i + 1]);
-          if (from == lane && !norm) out[i] = in[i];  // copied bit for bit, NaN included
+        for (int i = 0; i < 8; ++i) {
+          own[i] = c[i] * w[i];
+          other[i] = sign * s[i] * wp[i];
         }
       }
-      if (active && h < a.H)
-        *reinterpret_cast<uint4*>(is_q ? qo + h * a.q.out_h : ko + (h - a.Hq) * a.k.out_h) =
-            make_uint4(out[0], out[1], out[2], out[3]);
+      const int steps = H > part * kHeads ? (H - part * kHeads + step - 1) / step : 0;
+      walk.run(norm, inv_d, a.eps, own, other, from, copy, steps);
     }
-    if (h0 + kRopeBatch * step < a.H) load(mine + kRopeBatch * step);
+    bar_sync(1 + slot, parts * 32);                  // the angles have been read
+    t += static_cast<int64_t>(gridDim.x) * tokens;
+    if (t < a.T) begin();                            // in flight while the next angles are formed
   }
 }
 
 template <class T>
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   const int lph = a.D <= 64 ? 8 : (a.D <= 128 ? 16 : 32);
-  // warps per token: all eight for few tokens (latency), else as many as leave
-  // each warp a batch of loads
-  int wpt = 8;
-  if (a.T > 1184)
-    while (wpt > 1 && a.H * lph < wpt * 32 * kRopeBatch) wpt /= 2;
-  const int tokens = kRopeWarps / wpt;
+  // Warps per token.  A warp's time is about that of its head steps plus four
+  // more for the angles and the rest of a token, and the tokens run in rounds
+  // of what the GPU holds: take the number that costs least (one or two for
+  // many tokens, as many as have heads to take for few).
+  const int heads = 32 / lph, Hk = a.H - a.Hq;
+  const int64_t most = static_cast<int64_t>(num_sms) * rope_blocks(a.interleaved != 0, a.R < a.D);
+  int parts = 1;
+  int64_t best = INT64_MAX;
+  for (int p = 1; p <= kRopeWarps; p *= 2) {
+    const int64_t at_once = most * (kRopeWarps / p);
+    const int64_t rounds = (a.T + at_once - 1) / at_once;
+    const int64_t cost = rounds * (4 + (a.Hq + p * heads - 1) / (p * heads) + (Hk + p * heads - 1) / (p * heads));
+    if (cost < best) best = cost, parts = p;
+  }
+  const int tokens = kRopeWarps / parts;
+  const int64_t blocks = (a.T + tokens - 1) / tokens;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most), 1, 1);
   cfg.blockDim = dim3(kRopeThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -229,14 +339,21 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (a.interleaved) {
-    if (lph == 8) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 8, true>, a, wpt);
-    if (lph == 16) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 16, true>, a, wpt);
-    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 32, true>, a, wpt);
+  const int which = (lph == 8 ? 0 : lph == 16 ? 4 : 8) + (a.interleaved ? 2 : 0) + (a.R < a.D ? 1 : 0);
+  switch (which) {
+    case 0: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 8, false, false>, a, parts);
+    case 1: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 8, false, true>, a, parts);
+    case 2: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 8, true, false>, a, parts);
+    case 3: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 8, true, true>, a, parts);
+    case 4: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 16, false, false>, a, parts);
+    case 5: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 16, false, true>, a, parts);
+    case 6: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 16, true, false>, a, parts);
+    case 7: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 16, true, true>, a, parts);
+    case 8: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 32, false, false>, a, parts);
+    case 9: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 32, false, true>, a, parts);
+    case 10: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 32, true, false>, a, parts);
+    default: return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 32, true, true>, a, parts);
   }
-  if (lph == 8) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 8, false>, a, wpt);
-  if (lph == 16) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 16, false>, a, wpt);
-  return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<T, 32, false>, a, wpt);
 }
 
 int check_side(const void* in, int64_t in_t, int64_t in_h, const void* out, int64_t out_t, int64_t out_h,
@@ -306,6 +423,6 @@ extern "C" int w4a4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t 
   a.axis = axis;
   a.interleaved = interleaved != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == W4A4_BF16 ? launch_rope<Bf16>(a, s) : launch_rope<Fp16>(a, s);
+  const cudaError_t e = dtype == W4A4_BF16 ? launch_rope<Bf16>(a, dev->num_sms, s) : launch_rope<Fp16>(a, dev->num_sms, s);
   return e == cudaSuccess ? W4A4_OK : W4A4_ERR_CUDA;
 }
