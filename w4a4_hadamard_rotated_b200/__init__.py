@@ -387,30 +387,26 @@ def _need_16bit(t, name):
     return code
 
 
-def _same(t, dtype, shape, name, device):
-    """A contiguous operand of the given type and shape on the device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+def _same(t, dtype, shape, name, index):
+    """A contiguous operand of the given type and shape on CUDA device `index`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _call(fn, device, args, what):
-    """fn(*args, stream) with `device` current."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+def _call(fn, index, args, what):
+    """fn(*args, current stream of CUDA device `index`) with that device current."""
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != OK:
         raise W4A4Error(status, what)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def quantize_weight_w4a16(W, group=128, dtype=torch.bfloat16, asymmetric=False):
@@ -429,9 +425,9 @@ def quantize_weight_w4a16(W, group=128, dtype=torch.bfloat16, asymmetric=False):
     Wq = torch.empty(N, K // 2, dtype=torch.int8, device=W.device)
     scale = torch.empty(N, K // group, dtype=dtype, device=W.device)
     offset = torch.empty_like(scale) if asymmetric else None
-    _call(lib.w4a4_quantize_weight_w4a16, W.device,
-          (W.data_ptr(), N, K, W.stride(0), group, _DTYPES[dtype], Wq.data_ptr(), scale.data_ptr(), _addr(offset)),
-          "w4a4_quantize_weight_w4a16")
+    _call(lib.w4a4_quantize_weight_w4a16, W.get_device(),
+          (W.data_ptr(), N, K, W.stride(0), group, _DTYPES[dtype], Wq.data_ptr(), scale.data_ptr(),
+           offset.data_ptr() if asymmetric else None), "w4a4_quantize_weight_w4a16")
     return Wq, scale, offset
 
 
@@ -444,28 +440,25 @@ def linear_w4a16(x, Wq, scale, offset=None, bias=None, out=None):
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D tensor with a contiguous inner dimension")
     M, K = x.shape
-    dev, dtype = x.device, x.dtype
+    index, dtype = x.get_device(), x.dtype
     if not isinstance(Wq, torch.Tensor) or Wq.dim() != 2:
         raise ValueError("Wq must be a contiguous [N, K/2] int8 tensor on x's device")
     N = Wq.shape[0]
-    _same(Wq, torch.int8, (N, K // 2), "Wq", dev)
+    wp = _same(Wq, torch.int8, (N, K // 2), "Wq", index)
     if not isinstance(scale, torch.Tensor) or scale.dim() != 2 or scale.shape[1] < 1 or K % scale.shape[1] != 0:
         raise ValueError("scale must be a [N, K/group] tensor")
     groups = scale.shape[1]
-    _same(scale, dtype, (N, groups), "scale", dev)
-    if offset is not None:
-        _same(offset, dtype, (N, groups), "offset", dev)
-    if bias is not None:
-        _same(bias, dtype, (N,), "bias", dev)
+    sp = _same(scale, dtype, (N, groups), "scale", index)
+    op = None if offset is None else _same(offset, dtype, (N, groups), "offset", index)
+    bp = None if bias is None else _same(bias, dtype, (N,), "bias", index)
     if out is None:
-        y = torch.empty((M, N), dtype=dtype, device=dev)
+        out = x.new_empty((M, N))
     else:
-        y = out
-        _need_rows(y, dtype, M, N, "out", dev)
-    _call(lib.w4a4_linear_w4a16, dev,
-          (x.data_ptr(), x.stride(0) if M > 1 else K, Wq.data_ptr(), scale.data_ptr(), _addr(offset), K // groups,
-           _addr(bias), y.data_ptr(), y.stride(0) if M > 1 else N, M, N, K, code), "w4a4_linear_w4a16")
-    return y
+        _need_rows(out, dtype, M, N, "out", x.device)
+    _call(lib.w4a4_linear_w4a16, index,
+          (x.data_ptr(), x.stride(0) if M > 1 else K, wp, sp, op, K // groups, bp, out.data_ptr(),
+           out.stride(0) if M > 1 else N, M, N, K, code), "w4a4_linear_w4a16")
+    return out
 
 
 def rotary_frequencies(axis_dims, theta=10000.0, device="cuda"):
@@ -483,14 +476,43 @@ def rotary_frequencies(axis_dims, theta=10000.0, device="cuda"):
             torch.tensor(axis, dtype=torch.int32, device=device))
 
 
-def _heads(t, name, T, H, D, dtype, device):
-    """Strides (token, head) of a [T, H, D] tensor with contiguous D; a
-    dimension of one or no element has no stride of its own."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
-        raise TypeError(f"{name} must be a CUDA tensor of {dtype} on {device}")
-    if t.dim() != 3 or t.shape != (T, H, D) or (t.stride(2) != 1 and t.numel()):
-        raise ValueError(f"{name} must be [{T}, {H}, {D}] with a contiguous last dimension, got {tuple(t.shape)}")
-    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
+def _heads(t, name, T, H, D, dtype, index):
+    """(address, token stride, head stride) of a [T, H, D] tensor with
+    contiguous D; a dimension of one or no element has no stride of its own."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype} on cuda:{index}")
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.numel():
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return t.data_ptr(), st if T > 1 else H * D, sh if H > 1 else D
+
+
+def _positions(positions, freq, axis, T, index):
+    """(positions, bits, row stride, axes, freq, axis, R) for the library."""
+    if not isinstance(positions, torch.Tensor) or positions.get_device() != index:
+        raise TypeError("positions must be a CUDA tensor on q's device")
+    if positions.dtype is torch.int32:
+        bits = 32
+    elif positions.dtype is torch.int64:
+        bits = 64
+    else:
+        raise TypeError(f"positions must be torch.int32 or torch.int64, got {positions.dtype}")
+    if positions.dim() not in (1, 2) or positions.shape[0] != T:
+        raise ValueError(f"positions must be [{T}, axes] or [{T}], got {tuple(positions.shape)}")
+    axes = positions.shape[1] if positions.dim() == 2 else 1
+    if axes > 1 and positions.stride(1) != 1:
+        raise ValueError("positions must have a contiguous inner dimension")
+    if freq is None or axis is None:
+        raise ValueError("positions need freq and axis (rotary_frequencies)")
+    half = freq.numel()
+    return (positions.data_ptr(), bits, positions.stride(0) if T > 1 else axes, axes,
+            _same(freq, torch.float64, (half,), "freq", index), _same(axis, torch.int32, (half,), "axis", index),
+            2 * half)
+
+
+_NO_POSITIONS = (None, 0, 0, 0, None, None, 0)
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, freq=None, axis=None, interleaved=True,
@@ -507,55 +529,33 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, freq=N
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D]")
     T, Hq, D = q.shape
-    dev, dtype = q.device, q.dtype
-    qt, qh = _heads(q, "q", T, Hq, D, dtype, dev)
+    index, dtype = q.get_device(), q.dtype
+    qp, qt, qh = _heads(q, "q", T, Hq, D, dtype, index)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
-        qot, qoh = Hq * D, D
+        q_out = q.new_empty((T, Hq, D))
+        qo = (q_out.data_ptr(), Hq * D, D)
     else:
-        qot, qoh = _heads(q_out, "q_out", T, Hq, D, dtype, dev)
-    Hk, kt, kh, kot, koh = 0, 0, 0, 0, 0
+        qo = _heads(q_out, "q_out", T, Hq, D, dtype, index)
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 3:
             raise ValueError("k must be [T, Hk, D]")
         Hk = k.shape[1]
-        kt, kh = _heads(k, "k", T, Hk, D, dtype, dev)
+        kp, kt, kh = _heads(k, "k", T, Hk, D, dtype, index)
         if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
-            kot, koh = Hk * D, D
+            k_out = k.new_empty((T, Hk, D))
+            ko = (k_out.data_ptr(), Hk * D, D)
         else:
-            kot, koh = _heads(k_out, "k_out", T, Hk, D, dtype, dev)
+            ko = _heads(k_out, "k_out", T, Hk, D, dtype, index)
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    if q_weight is not None:
-        _same(q_weight, dtype, (D,), "q_weight", dev)
-    if k_weight is not None:
-        _same(k_weight, dtype, (D,), "k_weight", dev)
-    bits, pt, axes, R = 0, 0, 0, 0
-    if positions is not None:
-        if not isinstance(positions, torch.Tensor) or positions.device != dev:
-            raise TypeError("positions must be a CUDA tensor on q's device")
-        if positions.dtype == torch.int32:
-            bits = 32
-        elif positions.dtype == torch.int64:
-            bits = 64
-        else:
-            raise TypeError(f"positions must be torch.int32 or torch.int64, got {positions.dtype}")
-        axes = positions.shape[1] if positions.dim() == 2 else 1
-        if positions.dim() not in (1, 2) or positions.shape[0] != T:
-            raise ValueError(f"positions must be [{T}, axes] or [{T}], got {tuple(positions.shape)}")
-        if positions.dim() == 2 and axes > 1 and positions.stride(1) != 1:
-            raise ValueError("positions must have a contiguous inner dimension")
-        pt = positions.stride(0) if T > 1 else axes
-        if freq is None or axis is None:
-            raise ValueError("positions need freq and axis (rotary_frequencies)")
-        R = 2 * freq.numel()
-        _same(freq, torch.float64, (R // 2,), "freq", dev)
-        _same(axis, torch.int32, (R // 2,), "axis", dev)
-    _call(lib.w4a4_qk_norm_rope, dev,
-          (q.data_ptr(), qt, qh, Hq, _addr(k), kt, kh, Hk, _addr(q_weight), _addr(k_weight), eps, _addr(positions),
-           bits, pt, axes, _addr(freq), _addr(axis), R, 1 if interleaved else 0, q_out.data_ptr(), qot, qoh,
-           _addr(k_out), kot, koh, T, D, code), "w4a4_qk_norm_rope")
+    else:
+        Hk, kp, kt, kh, ko = 0, None, 0, 0, (None, 0, 0)
+    _call(lib.w4a4_qk_norm_rope, index,
+          (qp, qt, qh, Hq, kp, kt, kh, Hk,
+           None if q_weight is None else _same(q_weight, dtype, (D,), "q_weight", index),
+           None if k_weight is None else _same(k_weight, dtype, (D,), "k_weight", index), eps,
+           *(_NO_POSITIONS if positions is None else _positions(positions, freq, axis, T, index)),
+           1 if interleaved else 0, *qo, *ko, T, D, code), "w4a4_qk_norm_rope")
     return q_out, k_out
 
 
@@ -575,35 +575,35 @@ def attention(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, causal=False, scale
     if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("q must be [Tq, Hq, D] and k, v [Tk, Hk, D]")
     Tq, Hq, D = q.shape
-    Tk, Hk = k.shape[0], k.shape[1]
-    dev, dtype = q.device, q.dtype
-    qt, qh = _heads(q, "q", Tq, Hq, D, dtype, dev)
-    kt, kh = _heads(k, "k", Tk, Hk, D, dtype, dev)
-    vt, vh = _heads(v, "v", Tk, Hk, D, dtype, dev)
+    Tk, Hk, _ = k.shape
+    index, dtype = q.get_device(), q.dtype
+    qs = _heads(q, "q", Tq, Hq, D, dtype, index)
+    ks = _heads(k, "k", Tk, Hk, D, dtype, index)
+    vs = _heads(v, "v", Tk, Hk, D, dtype, index)
     if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=dtype, device=dev)
-        ot, oh = Hq * D, D
+        out = q.new_empty((Tq, Hq, D))
+        os_ = (out.data_ptr(), Hq * D, D)
     else:
-        ot, oh = _heads(out, "out", Tq, Hq, D, dtype, dev)
-    B = 1
+        os_ = _heads(out, "out", Tq, Hq, D, dtype, index)
+    B, cq, ck = 1, None, None
     if cu_seqlens_q is not None or cu_seqlens_k is not None:
         if cu_seqlens_q is None or cu_seqlens_k is None:
             raise ValueError("cu_seqlens_q and cu_seqlens_k go together")
         B = cu_seqlens_q.numel() - 1
         if B < 1:
             raise ValueError("cu_seqlens_q must hold at least two numbers")
-        _same(cu_seqlens_q, torch.int32, (B + 1,), "cu_seqlens_q", dev)
-        _same(cu_seqlens_k, torch.int32, (B + 1,), "cu_seqlens_k", dev)
-    lse = torch.empty((Tq, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    # the workspace is the caller's own and lives in PyTorch's allocator (or a
+        cq = _same(cu_seqlens_q, torch.int32, (B + 1,), "cu_seqlens_q", index)
+        ck = _same(cu_seqlens_k, torch.int32, (B + 1,), "cu_seqlens_k", index)
+    lse = q.new_empty((Tq, Hq), dtype=torch.float32) if return_lse else None
+    # the workspace is this call's own and lives in PyTorch's allocator (or a
     # graph's pool) until the stream is past it, so overlapping calls and
     # captured graphs never share one
     nbytes = lib.w4a4_attention_workspace_bytes(Tq, Tk, B, Hq, Hk, D)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    _call(lib.w4a4_attention, dev,
-          (q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot, oh, _addr(lse),
-           _addr(cu_seqlens_q), _addr(cu_seqlens_k), B, Tq, Tk, Hq, Hk, D, 1 if causal else 0,
-           D ** -0.5 if scale is None else float(scale), code, _addr(ws), nbytes), "w4a4_attention")
+    ws = q.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    _call(lib.w4a4_attention, index,
+          (*qs, *ks, *vs, *os_, None if lse is None else lse.data_ptr(), cq, ck, B, Tq, Tk, Hq, Hk, D,
+           1 if causal else 0, D ** -0.5 if scale is None else float(scale), code,
+           None if ws is None else ws.data_ptr(), nbytes), "w4a4_attention")
     return (out, lse) if return_lse else out
 
 
