@@ -93,18 +93,29 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------ product
 constexpr int kW16Warps = 8;
 
+// (w & mask) ^ magic
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(v) : "r"(w), "r"(mask), "r"(magic));
+  return v;
+}
+
 template <class T>
 struct Widen;
 template <>
 struct Widen<Bf16> {
-  // the codes at bits 0..3 and 16..19 of w, as bf16 integers
   static __device__ __forceinline__ uint32_t pair(uint32_t w) {
-    uint32_t v, r;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(v) : "r"(w), "r"(0x000F000Fu), "r"(0x43084308u));   // (w & mask) ^ magic
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                     __floats2bfloat162_rn(136.f, 136.f));
-    r = *reinterpret_cast<const uint32_t*>(&d);
-    return r;
+    const uint32_t v = and_xor(w, 0x000F000Fu, 0x43084308u);          // 136 + q
+    const __nv_bfloat162 d =
+        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __floats2bfloat162_rn(136.f, 136.f));
+    return *reinterpret_cast<const uint32_t*>(&d);
+  }
+  // codes 0 and 4, 1 and 5, 2 and 6, 3 and 7 of a word as pairs of integers
+  static __device__ __forceinline__ void word(uint32_t w, uint32_t (&p)[4]) {
+    p[0] = pair(w);
+    p[1] = pair(w >> 4);
+    p[2] = pair(w >> 8);
+    p[3] = pair(w >> 12);
   }
   static constexpr uint32_t kOnes = 0x3F803F80u;
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -112,20 +123,43 @@ struct Widen<Bf16> {
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
+  static __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  }
 };
 template <>
 struct Widen<Fp16> {
-  static __device__ __forceinline__ uint32_t pair(uint32_t w) {
-    uint32_t v;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(v) : "r"(w), "r"(0x000F000Fu), "r"(0x64086408u));
+  // the low nibbles of the bytes: 1032 + q;  the high ones where they lie, 16
+  // times as large: 1024 + 16 (q + 8) = 1152 + 16 q, one multiply-add (exact)
+  static __device__ __forceinline__ uint32_t low(uint32_t w) {
+    const uint32_t v = and_xor(w, 0x000F000Fu, 0x64086408u);
     const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(1032.f, 1032.f));
     return *reinterpret_cast<const uint32_t*>(&d);
+  }
+  static __device__ __forceinline__ uint32_t high(uint32_t w) {
+    const uint32_t v = and_xor(w, 0x00F000F0u, 0x64806480u);
+    const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(0.0625f, 0.0625f),
+                              __floats2half2_rn(-72.f, -72.f));
+    return *reinterpret_cast<const uint32_t*>(&d);
+  }
+  static __device__ __forceinline__ void word(uint32_t w, uint32_t (&p)[4]) {
+    p[0] = low(w);
+    p[1] = high(w);
+    p[2] = low(w >> 8);
+    p[3] = high(w >> 8);
   }
   static constexpr uint32_t kOnes = 0x3C003C00u;
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  static __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
   }
 };
 
@@ -136,76 +170,89 @@ struct W16Args {
   uint16_t* y;
   int64_t ldy;
   int M, N, K;
-  int split;           // CTAs of a cluster, each with a slice of k
+  int tiles;           // sets of RT * 16 rows
   unsigned int* status;
   unsigned long long wait_ns;
 };
 
-template <int RT, int NT>
+constexpr int kW16Scales = 16;       // groups of a row whose scales a warp holds at a time
+constexpr int kW16Pitch = 18;        // and their row pitch in shared memory: 9 words, rows on different banks
+
+// FEW: one or two activation rows.
+template <int RT, int NT, bool FEW, bool OFFSET>
 struct W16Shape {
-  static constexpr int kRows = RT * 16, kCols = NT * 8;
+  static constexpr int kRows = RT * 16;
+  static constexpr int kCols = FEW ? 2 : NT * 8;             // columns of a partial sum
   static constexpr uint32_t kW = kRows * 64;                 // codes of a stage
   // x of a stage: two boxes of 64 columns, 128-byte swizzle; for one or two
-  // rows (RT == 1) one unswizzled box of 128 columns
-  static constexpr uint32_t kXBox = RT == 1 ? 512 : NT * 1024;
-  static constexpr uint32_t kX = RT == 1 ? 512 : 2 * kXBox;
-  static constexpr uint32_t kStage = kW + kX;               // a multiple of the swizzle pattern: 512 bytes (RT == 1), 1024
-  static constexpr int kStages = RT == 1 ? 5 : (NT == 1 ? 3 : 2);
+  // rows one unswizzled box of 128 columns
+  static constexpr uint32_t kXBox = FEW ? 512 : NT * 1024;
+  static constexpr uint32_t kX = FEW ? 512 : 2 * kXBox;
+  static constexpr uint32_t kStage = kW + kX;          // a multiple of the swizzles' period: 512 bytes, with x swizzled 1024
+  static constexpr int kStages = FEW ? 4 : (RT * NT == 2 ? 2 : 2);
+  static constexpr uint32_t kScale = kRows * kW16Pitch * 2;  // of one chunk
+  static constexpr uint32_t kWarp = (OFFSET ? 4 : 2) * kScale;
+  static constexpr uint32_t kPart = kW16Warps * kRows * kCols * sizeof(float);
   static constexpr uint32_t kRing = kW16Warps * kStages * kStage;
-  static constexpr uint32_t kParts = (kW16Warps + 1) * kRows * kCols * sizeof(float);
-  static constexpr uint32_t kSmem = (kRing > kParts ? kRing : kParts) + 1024;
+  static constexpr uint32_t kSmem = kRing + 2 * kPart + kW16Warps * kWarp + 1024;
+  static constexpr int kBlocks = kSmem <= 113 * 1024 ? 2 : 1;
 };
 
-// The scales (or offsets) of a row's groups in a stage: kW16Cols / GROUP
-// 16-bit numbers from `at` on, those past the row's last group are that group's.
-template <int GROUP>
-struct Scales {
-  static constexpr int kCount = kW16Cols / GROUP;
-  uint32_t w[kCount == 4 ? 2 : 1];
-  __device__ __forceinline__ void load(const uint16_t* row, int at, int groups, bool wide) {
-    if (kCount == 1) {
-      w[0] = row[min(at, groups - 1)];
-    } else if (wide) {                                 // rows of an even number of 4 or 8 bytes
-      if (kCount == 2) {
-        w[0] = *reinterpret_cast<const uint32_t*>(row + min(at, groups - 2));
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(row + min(at, groups - 4));
-        w[0] = v.x;
-        w[kCount == 4 ? 1 : 0] = v.y;
-      }
-    } else {
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+// Scales (or offsets) first .. first + count - 1 of a warp's rows into shared
+// memory, [row][kW16Pitch]: where rows are whole 32-bit words as asynchronous
+// copies of the words that hold them, else loaded and stored here.  Returns
+// nothing to wait for but cp_async_wait().  Rows past N take the last one's.
+template <int ROWS>
+__device__ __forceinline__ void fetch_scales(uint16_t* to, const uint16_t* from, int row0, int N, int groups, int first,
+                                             int count, bool words) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = 32 / (ROWS < 32 ? ROWS : 32);       // lanes of a row
+  const int last = min(first + count, groups) - 1;
 #pragma unroll
-      for (int i = 0; i < kCount; i += 2)
-        w[i / 2] = row[min(at + i, groups - 1)] | static_cast<uint32_t>(row[min(at + i + 1, groups - 1)]) << 16;
+  for (int r = 0; r < ROWS; r += 32 / kLanes) {
+    const int row = r + lane / kLanes;
+    const uint16_t* src = from + static_cast<int64_t>(min(row0 + row, N - 1)) * groups;
+    uint16_t* dst = to + row * kW16Pitch;
+    if (words) {
+      const int w0 = first / 2;
+      for (int w = w0 + lane % kLanes; w <= last / 2; w += kLanes) cp_async4(smem_u32(dst + 2 * (w - w0)), src + 2 * w);
+    } else {
+      const int g0 = first & ~1;
+      for (int g = first + lane % kLanes; g <= last; g += kLanes) dst[g - g0] = src[g];
     }
   }
-  template <class T>
-  __device__ __forceinline__ float get(int i) const {
-    return T::to_f32(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1))));
-  }
-};
+}
 
-// grid.x = row tile sets * split; 8 warps.
-template <class T, int RT, int NT, int GROUP, bool OFFSET>
-__global__ void __launch_bounds__(kW16Warps * 32, 2)
+// A persistent grid over sets of RT * 16 weight rows; 8 warps, each with its slice of k.
+template <class T, int RT, int NT, bool FEW, int GROUP, bool OFFSET>
+__global__ void __launch_bounds__(kW16Warps * 32, W16Shape<RT, NT, FEW, OFFSET>::kBlocks)
     linear_w4a16_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const W16Args a) {
-  using Shape = W16Shape<RT, NT>;
+  using Shape = W16Shape<RT, NT, FEW, OFFSET>;
   constexpr int kRows = Shape::kRows, kCols = Shape::kCols, kStages = Shape::kStages;
-  constexpr int kGroups = kW16Cols / GROUP;
+  constexpr int kGroups = kW16Cols / GROUP;            // groups of a stage
+  constexpr int kEvery = kW16Scales / kGroups;         // stages whose scales are held at a time
   extern __shared__ uint8_t smem_dyn[];
   __shared__ uint64_t full[kW16Warps][kStages];
   uint8_t* smem = align1024_shared(smem_dyn);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int rank = static_cast<int>(blockIdx.x) % a.split;
-  const int row0 = static_cast<int>(blockIdx.x) / a.split * kRows;
   const int groups = a.K / GROUP;
   // this warp's stages of k
-  const int units = (a.K + kW16Cols - 1) / kW16Cols, shares = a.split * kW16Warps, share = rank * kW16Warps + warp;
-  const int u0 = static_cast<int>(static_cast<int64_t>(units) * share / shares);
-  const int n = static_cast<int>(static_cast<int64_t>(units) * (share + 1) / shares) - u0;
+  const int units = (a.K + kW16Cols - 1) / kW16Cols;
+  const int u0 = units * warp / kW16Warps, n = units * (warp + 1) / kW16Warps - u0;
   uint8_t* ring = smem + warp * kStages * Shape::kStage;
+  float* part = reinterpret_cast<float*>(smem + Shape::kRing);            // [2][warps][kRows][kCols]
+  uint16_t* scales = reinterpret_cast<uint16_t*>(smem + Shape::kRing + 2 * Shape::kPart + warp * Shape::kWarp);
+  const bool words = groups % 2 == 0 &&
+                     ((reinterpret_cast<uintptr_t>(a.scale) | reinterpret_cast<uintptr_t>(a.offset)) & 3) == 0;
 
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&full[warp][s], 1);
@@ -218,176 +265,170 @@ __global__ void __launch_bounds__(kW16Warps * 32, 2)
   griddep_wait();
   griddep_launch_dependents();
 
-  auto issue = [&](int i) {                            // lane 0
-    const int s = i % kStages, col = (u0 + i) * kW16Cols;
-    uint8_t* at = ring + s * Shape::kStage;
-    mbar_arrive_expect_tx(&full[warp][s], Shape::kW + static_cast<uint32_t>(a.M) * 256u);
-    tma_load_2d(at, &tmW, &full[warp][s], col / 2, row0);
-    tma_load_2d(at + Shape::kW, &tmX, &full[warp][s], col, 0);
-    if (RT > 1) tma_load_2d(at + Shape::kW + Shape::kXBox, &tmX, &full[warp][s], col + 64, 0);
+  // ---- the two streams ahead of the sums: stages (lane 0, by TMA) and chunks of scales
+  int in_tile = blockIdx.x, in_i = 0, in_s = 0;
+  auto issue = [&] {                                   // lane 0
+    if (in_tile >= a.tiles || n == 0) return;
+    const int col = (u0 + in_i) * kW16Cols;
+    uint8_t* at = ring + in_s * Shape::kStage;
+    uint64_t* bar = &full[warp][in_s];
+    mbar_arrive_expect_tx(bar, Shape::kW + static_cast<uint32_t>(a.M) * 256u);
+    tma_load_2d(at, &tmW, bar, col / 2, in_tile * kRows);
+    tma_load_2d(at + Shape::kW, &tmX, bar, col, 0);
+    if (!FEW) tma_load_2d(at + Shape::kW + Shape::kXBox, &tmX, bar, col + 64, 0);
+    if (++in_s == kStages) in_s = 0;
+    if (++in_i == n) in_i = 0, in_tile += gridDim.x;
+  };
+  int sc_tile = blockIdx.x, sc_i = 0, sc_b = 0;        // the next chunk to fetch, and its buffer
+  auto fetch = [&] {
+    if (sc_tile >= a.tiles || n == 0) return;
+    const int first = (u0 + sc_i) * kGroups, count = min(kEvery, n - sc_i) * kGroups;
+    uint16_t* to = scales + sc_b * (Shape::kScale / 2);
+    fetch_scales<kRows>(to, a.scale, sc_tile * kRows, a.N, groups, first, count, words);
+    if (OFFSET) fetch_scales<kRows>(to + Shape::kScale, a.offset, sc_tile * kRows, a.N, groups, first, count, words);
+    sc_b ^= 1;
+    sc_i += kEvery;
+    if (sc_i >= n) sc_i = 0, sc_tile += gridDim.x;
   };
   if (lane == 0)
-    for (int i = 0; i < kStages && i < n; ++i) issue(i);
+    for (int i = 0; i < kStages; ++i) issue();
+  fetch();
 
-  // rows past N take the last row's scales; their codes are zeros and their results dropped
-  const uint16_t *srow[RT][2], *orow[RT][2];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t row = min(row0 + 16 * i + 8 * h + g, a.N - 1);
-      srow[i][h] = a.scale + row * groups;
-      if (OFFSET) orow[i][h] = a.offset + row * groups;
-    }
-  const bool wide = groups % kGroups == 0 &&
-                    ((reinterpret_cast<uintptr_t>(a.scale) | reinterpret_cast<uintptr_t>(a.offset)) & (2 * kGroups - 1)) == 0;
-  Scales<GROUP> sc[RT][2], of[RT][2];
-  auto load_scales = [&](int i) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sc[r][h].load(srow[r][h], (u0 + i) * kGroups, groups, wide);
-        if (OFFSET) of[r][h].load(orow[r][h], (u0 + i) * kGroups, groups, wide);
-      }
-  };
-  float acc[RT][NT][4] = {};
-  if (n > 0) load_scales(0);
+  int s = 0, buf = 0, sb = 0;
+  uint32_t phase = 0;
   bool ok = true;
-
-  for (int i = 0; i < n; ++i) {
-    const int s = i % kStages;
-    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[warp][s], (i / kStages) & 1, nullptr, a.status, a.wait_ns));
-    if (!ok) break;
-    const uint32_t wbase = smem_u32(ring + s * Shape::kStage), xbase = wbase + Shape::kW;
-    const Scales<GROUP>(&s0)[RT][2] = sc;
-    float sf[RT][2][kGroups], of32[RT][2][kGroups];
+  for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    const int row0 = tile * kRows;
+    float acc[RT][NT][4] = {};
+    const uint16_t *sc = scales, *of = scales;
+    for (int i = 0; i < n && ok; ++i) {
+      if (i % kEvery == 0) {                           // this chunk has arrived, the next one sets off
+        cp_async_wait();
+        __syncwarp();
+        const int skip = ((u0 + i) * kGroups) & 1;
+        sc = scales + sb * (Shape::kScale / 2) + skip;
+        of = sc + Shape::kScale;
+        sb ^= 1;
+        fetch();
+      }
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[warp][s], phase, nullptr, a.status, a.wait_ns));
+      if (!ok) break;
+      const uint32_t wbase = smem_u32(ring + s * Shape::kStage), xbase = wbase + Shape::kW;
+      float sum[RT][NT][4], xs[NT][4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+      for (int k = 0; k < 2; ++k) {                    // 64 columns each
+        // x as the B operand: this lane's 16 elements of row 8 j + g, as pairs (0, 4), (1, 5), (2, 6), (3, 7)
+        uint32_t xb[NT][2][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < kGroups; ++e) {
-          sf[r][h][e] = s0[r][h].template get<T>(e);
-          of32[r][h][e] = OFFSET ? of[r][h].template get<T>(e) : 0.f;
-        }
-    if (i + 1 < n) load_scales(i + 1);
-    float sum[RT][NT][4] = {}, xs[NT][4] = {};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {                      // 64 columns each
-      // x as the B operand: this lane's 16 elements of row 8 j + g, as pairs (0, 4), (1, 5), (2, 6), (3, 7)
-      uint32_t xb[NT][2][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          // which eight columns: with groups of 32 the order after the swap below
-          const int c = GROUP < 64 ? (4 * v | (t & 1) << 1 | t >> 1) : 2 * t + v;
-          uint4 q = make_uint4(0u, 0u, 0u, 0u);
-          if (8 * j + g < a.M) {
-            if (RT == 1) q = lds128(xbase + g * 256 + k * 128 + c * 16);
-            else q = lds128(xbase + k * Shape::kXBox + (8 * j + g) * 128 + ((c ^ g) << 4));
+          for (int v = 0; v < 2; ++v) {
+            // which eight columns: with groups of 32 the order after the swap below
+            const int c = GROUP < 64 ? (4 * v | (t & 1) << 1 | t >> 1) : 2 * t + v;
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (8 * j + g < a.M) {
+              if (FEW) q = lds128(xbase + g * 256 + k * 128 + c * 16);
+              else q = lds128(xbase + k * Shape::kXBox + (8 * j + g) * 128 + ((c ^ g) << 4));
+            }
+            xb[j][v][0] = __byte_perm(q.x, q.z, 0x5410);
+            xb[j][v][1] = __byte_perm(q.x, q.z, 0x7632);
+            xb[j][v][2] = __byte_perm(q.y, q.w, 0x5410);
+            xb[j][v][3] = __byte_perm(q.y, q.w, 0x7632);
           }
-          xb[j][v][0] = __byte_perm(q.x, q.z, 0x5410);
-          xb[j][v][1] = __byte_perm(q.x, q.z, 0x7632);
-          xb[j][v][2] = __byte_perm(q.y, q.w, 0x5410);
-          xb[j][v][3] = __byte_perm(q.y, q.w, 0x7632);
-        }
-      uint2 w[RT][2];
+        uint2 w[RT][2];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = 16 * r + 8 * h + g, chunk = 2 * k + (t >> 1);
-          w[r][h] = lds64(wbase + row * 64 + ((chunk ^ (row >> 1 & 3)) << 4) + 8 * (t & 1));
-          if (GROUP < 64) {                            // lanes 0, 1 give their second word for the first of lanes 2, 3
-            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, t < 2 ? w[r][h].y : w[r][h].x, 2);
-            if (t < 2) w[r][h].y = got; else w[r][h].x = got;
+          for (int h = 0; h < 2; ++h) {
+            const int row = 16 * r + 8 * h + g, chunk = 2 * k + (t >> 1);
+            w[r][h] = lds64(wbase + row * 64 + ((chunk ^ (row >> 1 & 3)) << 4) + 8 * (t & 1));
+            if (GROUP < 64) {                          // lanes 0, 1 give their second word for the first of lanes 2, 3
+              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, t < 2 ? w[r][h].y : w[r][h].x, 2);
+              if (t < 2) w[r][h].y = got; else w[r][h].x = got;
+            }
           }
-        }
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {                    // 32 columns each
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
+        for (int v = 0; v < 2; ++v) {                  // 32 columns each
+          const int col = 64 * k + 32 * v;             // of the stage
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            const uint32_t lo = v == 0 ? w[r][0].x : w[r][0].y, hi = v == 0 ? w[r][1].x : w[r][1].y;
-            const uint32_t A[4] = {Widen<T>::pair(lo >> (8 * p)), Widen<T>::pair(hi >> (8 * p)),
-                                   Widen<T>::pair(lo >> (8 * p + 4)), Widen<T>::pair(hi >> (8 * p + 4))};
+            uint32_t lo[4], hi[4];
+            Widen<T>::word(v == 0 ? w[r][0].x : w[r][0].y, lo);
+            Widen<T>::word(v == 0 ? w[r][1].x : w[r][1].y, hi);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) Widen<T>::mma(sum[r][j], A, xb[j][v][2 * p], xb[j][v][2 * p + 1]);
+            for (int p = 0; p < 2; ++p) {
+              const uint32_t A[4] = {lo[2 * p], hi[2 * p], lo[2 * p + 1], hi[2 * p + 1]};
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                if (col % GROUP == 0 && p == 0) Widen<T>::mma_first(sum[r][j], A, xb[j][v][0], xb[j][v][1]);
+                else Widen<T>::mma(sum[r][j], A, xb[j][v][2 * p], xb[j][v][2 * p + 1]);
+              }
+            }
           }
           if (OFFSET) {
             const uint32_t ones[4] = {Widen<T>::kOnes, Widen<T>::kOnes, Widen<T>::kOnes, Widen<T>::kOnes};
 #pragma unroll
-            for (int j = 0; j < NT; ++j) Widen<T>::mma(xs[j], ones, xb[j][v][2 * p], xb[j][v][2 * p + 1]);
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                if (col % GROUP == 0 && p == 0) Widen<T>::mma_first(xs[j], ones, xb[j][v][0], xb[j][v][1]);
+                else Widen<T>::mma(xs[j], ones, xb[j][v][2 * p], xb[j][v][2 * p + 1]);
+              }
+          }
+          if ((col + 32) % GROUP == 0) {               // a group is done
+            const int e = min(i % kEvery * kGroups + col / GROUP, groups - 1 - (u0 + i - i % kEvery) * kGroups);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int at = (16 * r + 8 * h + g) * kW16Pitch + e;
+                const float sf = T::to_f32(sc[at]), o = OFFSET ? T::to_f32(of[at]) : 0.f;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int q = 2 * h; q < 2 * h + 2; ++q) {
+                    acc[r][j][q] = fmaf(sf, sum[r][j][q], acc[r][j][q]);
+                    if (OFFSET) acc[r][j][q] = fmaf(o, xs[j][q], acc[r][j][q]);
+                  }
+              }
           }
         }
-        const int col = 64 * k + 32 * v + 32;          // columns done
-        if (col % GROUP == 0) {
-          const int e = col / GROUP - 1;
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                acc[r][j][q] = fmaf(sf[r][q >> 1][e], sum[r][j][q], acc[r][j][q]);
-                if (OFFSET) acc[r][j][q] = fmaf(of32[r][q >> 1][e], xs[j][q], acc[r][j][q]);
-                sum[r][j][q] = 0.f;
-              }
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) xs[j][q] = 0.f;
-        }
       }
-    }
-    __syncwarp();                                      // every lane has read the stage
-    if (lane == 0 && i + kStages < n) issue(i + kStages);
-  }
-  if (!ok && lane == 0)                                // what is in flight lands before the memory is used again
-    for (int s = 0; s < kStages && s < n; ++s) {
-      (void)mbar_wait(&full[warp][s], 0, nullptr, nullptr, 100000000ull);
-      (void)mbar_wait(&full[warp][s], 1, nullptr, nullptr, 100000000ull);
+      __syncwarp();                                    // every lane has read the stage
+      if (lane == 0) issue();
+      if (++s == kStages) s = 0, phase ^= 1;
     }
 
-  // partial sums of the warps, joined in order; then those of the cluster
-  __syncthreads();                                     // the rings are free
-  float* part = reinterpret_cast<float*>(smem);        // [warps][kRows][kCols], then the CTA's [kRows][kCols]
+    // partial sums of the warps, joined in order; two buffers, so one barrier a tile
+    float* mine = part + (buf * kW16Warps + warp) * kRows * kCols;
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(&part[(warp * kRows + 16 * r + 8 * h + g) * kCols + 8 * j + 2 * t]) =
-            make_float2(acc[r][j][2 * h], acc[r][j][2 * h + 1]);
-  __syncthreads();
-  float* mine = part + kW16Warps * kRows * kCols;
-  for (int i = threadIdx.x; i < kRows * kCols; i += kW16Warps * 32) {
-    float v = 0.f;
+        for (int h = 0; h < 2; ++h)
+          if (!FEW || t == 0)
+            *reinterpret_cast<float2*>(&mine[(16 * r + 8 * h + g) * kCols + 8 * j + 2 * t]) =
+                make_float2(acc[r][j][2 * h], acc[r][j][2 * h + 1]);
+    __syncthreads();
+    // output i: row i % kRows, activation row i / kRows
+    for (int i = threadIdx.x; i < kRows * a.M; i += kW16Warps * 32) {
+      const int r = i % kRows, m = i / kRows, row = row0 + r;
+      const float* p = part + buf * kW16Warps * kRows * kCols + r * kCols + m;
+      if (row < a.N) {
+        float v = a.bias != nullptr ? T::to_f32(a.bias[row]) : 0.f;
 #pragma unroll
-    for (int w = 0; w < kW16Warps; ++w) v += part[w * kRows * kCols + i];
-    mine[i] = v;
-  }
-  if (a.split > 1) cluster_sync();
-  else __syncthreads();
-  // output i: row i % kRows, activation row i / kRows; the CTAs of a cluster share them out
-  for (int i = rank * kW16Warps * 32 + threadIdx.x; i < kRows * a.M; i += a.split * kW16Warps * 32) {
-    const int r = i % kRows, m = i / kRows, row = row0 + r;
-    float v = 0.f;
-    if (a.split > 1) {
-      for (int c = 0; c < a.split; ++c) v += ld_cluster(&mine[r * kCols + m], c);
-    } else {
-      v = mine[r * kCols + m];
+        for (int w = 0; w < kW16Warps; ++w) v += p[w * kRows * kCols];
+        a.y[m * a.ldy + row] = T::from_f32(v);
+      }
     }
-    if (row < a.N) {
-      if (a.bias != nullptr) v += T::to_f32(a.bias[row]);
-      a.y[m * a.ldy + row] = T::from_f32(v);
-    }
+    buf ^= 1;
   }
-  if (a.split > 1) cluster_sync();                     // nobody leaves while its sums are read
+  if (!ok && lane == 0)                                // an expired wait: what is in flight lands before the CTA ends
+    for (int i = 0; i < kStages; ++i) {
+      (void)mbar_wait(&full[warp][i], 0, nullptr, nullptr, 100000000ull);
+      (void)mbar_wait(&full[warp][i], 1, nullptr, nullptr, 100000000ull);
+    }
 }
 
 // The call's operands as the launcher takes them.
@@ -400,17 +441,17 @@ struct W16Call {
   cudaStream_t stream;
 };
 
-template <class T, int RT, int NT, int GROUP, bool OFFSET>
+template <class T, int RT, int NT, bool FEW, int GROUP, bool OFFSET>
 cudaError_t launch_w16(const W16Call& c, W16Args a) {
-  using Shape = W16Shape<RT, NT>;
+  using Shape = W16Shape<RT, NT, FEW, OFFSET>;
   CUtensorMap tmW, tmX;
   if (tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.wq, a.N, a.K / 2, a.K / 2, 64, Shape::kRows,
                     CU_TENSOR_MAP_SWIZZLE_64B) != W4A4_OK ||
       tensor_map_2d(&tmX, c.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.x, a.M, a.K,
-                    c.ldx * 2, RT == 1 ? 128 : 64, a.M,
-                    RT == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) != W4A4_OK)
+                    c.ldx * 2, FEW ? 128 : 64, a.M,
+                    FEW ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) != W4A4_OK)
     return cudaErrorInvalidValue;
-  auto kernel = linear_w4a16_kernel<T, RT, NT, GROUP, OFFSET>;
+  auto kernel = linear_w4a16_kernel<T, RT, NT, FEW, GROUP, OFFSET>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -423,34 +464,29 @@ cudaError_t launch_w16(const W16Call& c, W16Args a) {
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  const int64_t tiles = (a.N + Shape::kRows - 1) / Shape::kRows;
-  // slices of k: until there are two CTAs per SM, as long as a warp keeps a stage
-  const int64_t units = a.K / kW16Cols;
-  int split = 1;
-  while (split < 8 && tiles * split < 2 * c.num_sms && units >= 2 * split * kW16Warps) split *= 2;
-  a.split = split;
+  a.tiles = (a.N + Shape::kRows - 1) / Shape::kRows;
+  const int most = c.num_sms * Shape::kBlocks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.tiles < most ? a.tiles : most), 1, 1);
   cfg.blockDim = dim3(kW16Warps * 32, 1, 1);
   cfg.dynamicSmemBytes = Shape::kSmem;
   cfg.stream = c.stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, a);
 }
 
 template <class T, int GROUP, bool OFFSET>
 cudaError_t launch_w16_rows(const W16Call& c, const W16Args& a) {
-  if (a.M <= 2) return launch_w16<T, 1, 1, GROUP, OFFSET>(c, a);
-  if (a.M <= 8) return launch_w16<T, 2, 1, GROUP, OFFSET>(c, a);
-  return launch_w16<T, 2, 2, GROUP, OFFSET>(c, a);
+  if (a.M <= 2) {
+    if (a.N < 64 * c.num_sms) return launch_w16<T, 1, 1, true, GROUP, OFFSET>(c, a);
+    return launch_w16<T, 2, 1, true, GROUP, OFFSET>(c, a);
+  }
+  if (a.M <= 8) return launch_w16<T, 2, 1, false, GROUP, OFFSET>(c, a);
+  return launch_w16<T, 2, 2, false, GROUP, OFFSET>(c, a);
 }
 
 template <class T>
