@@ -91,8 +91,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------ product
-constexpr int kW16Warps = 8;
-
 // (w & mask) ^ magic
 __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t magic) {
   uint32_t v;
@@ -175,11 +173,8 @@ struct W16Args {
   unsigned long long wait_ns;
 };
 
-constexpr int kW16Scales = 16;       // groups of a row whose scales a warp holds at a time
-constexpr int kW16Pitch = 18;        // and their row pitch in shared memory: 9 words, rows on different banks
-
-// FEW: one or two activation rows.
-template <int RT, int NT, bool FEW, bool OFFSET>
+// FEW: one or two activation rows.  WARPS: of a CTA, which share k.
+template <int RT, int NT, bool FEW, int WARPS, bool OFFSET>
 struct W16Shape {
   static constexpr int kRows = RT * 16;
   static constexpr int kCols = FEW ? 2 : NT * 8;             // columns of a partial sum
@@ -189,29 +184,37 @@ struct W16Shape {
   static constexpr uint32_t kXBox = FEW ? 512 : NT * 1024;
   static constexpr uint32_t kX = FEW ? 512 : 2 * kXBox;
   static constexpr uint32_t kStage = kW + kX;          // a multiple of the swizzles' period: 512 bytes, with x swizzled 1024
-  static constexpr int kStages = FEW ? 4 : (RT * NT == 2 ? 2 : 2);
-  static constexpr uint32_t kScale = kRows * kW16Pitch * 2;  // of one chunk
+  static constexpr int kStages = FEW ? 3 : 2;
+  // groups of a row whose scales a warp holds at a time (with offsets, which
+  // take as much room again, half as many), and the row pitch that holds them
+  // from any beginning, rounded down to 8 groups
+  static constexpr int kHeld = OFFSET ? 8 : 16;
+  static constexpr int kPitch = kHeld + 8;
+  static constexpr uint32_t kScale = kRows * kPitch * 2;     // of one such chunk
   static constexpr uint32_t kWarp = (OFFSET ? 4 : 2) * kScale;
-  static constexpr uint32_t kPart = kW16Warps * kRows * kCols * sizeof(float);
-  static constexpr uint32_t kRing = kW16Warps * kStages * kStage;
-  static constexpr uint32_t kSmem = kRing + 2 * kPart + kW16Warps * kWarp + 1024;
-  static constexpr int kBlocks = kSmem <= 113 * 1024 ? 2 : 1;
+  static constexpr uint32_t kPart = WARPS * kRows * kCols * sizeof(float);
+  static constexpr uint32_t kRing = WARPS * kStages * kStage;
+  static constexpr uint32_t kSmem = kRing + kPart + WARPS * kWarp + 1024;
+  static_assert(kSmem <= 226 * 1024, "does not fit an SM's shared memory");
+  static constexpr int kBlocks = kSmem <= 113 * 1024 && WARPS <= 8 ? 2 : 1;
 };
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
 // Scales (or offsets) first .. first + count - 1 of a warp's rows into shared
-// memory, [row][kW16Pitch]: where rows are whole 32-bit words as asynchronous
-// copies of the words that hold them, else loaded and stored here.  Returns
-// nothing to wait for but cp_async_wait().  Rows past N take the last one's.
-template <int ROWS>
+// memory, [row][PITCH], beginning at first rounded down to `unit` groups:
+// where rows are whole units of 16 (unit 8) or 4 bytes (unit 2) as asynchronous
+// copies, to be waited for by cp_async_wait(), else loaded and stored here.
+// Rows past N take the last one's.
+template <int ROWS, int PITCH>
 __device__ __forceinline__ void fetch_scales(uint16_t* to, const uint16_t* from, int row0, int N, int groups, int first,
-                                             int count, bool words) {
+                                             int count, int unit) {
   const int lane = threadIdx.x & 31;
   constexpr int kLanes = 32 / (ROWS < 32 ? ROWS : 32);       // lanes of a row
   const int last = min(first + count, groups) - 1;
@@ -219,40 +222,42 @@ __device__ __forceinline__ void fetch_scales(uint16_t* to, const uint16_t* from,
   for (int r = 0; r < ROWS; r += 32 / kLanes) {
     const int row = r + lane / kLanes;
     const uint16_t* src = from + static_cast<int64_t>(min(row0 + row, N - 1)) * groups;
-    uint16_t* dst = to + row * kW16Pitch;
-    if (words) {
-      const int w0 = first / 2;
-      for (int w = w0 + lane % kLanes; w <= last / 2; w += kLanes) cp_async4(smem_u32(dst + 2 * (w - w0)), src + 2 * w);
+    uint16_t* dst = to + row * PITCH;
+    const int g0 = first & -unit;
+    if (unit == 8) {
+      for (int g = g0 + 8 * (lane % kLanes); g <= last; g += 8 * kLanes) cp_async<16>(smem_u32(dst + (g - g0)), src + g);
+    } else if (unit == 2) {
+      for (int g = g0 + 2 * (lane % kLanes); g <= last; g += 2 * kLanes) cp_async<4>(smem_u32(dst + (g - g0)), src + g);
     } else {
-      const int g0 = first & ~1;
-      for (int g = first + lane % kLanes; g <= last; g += kLanes) dst[g - g0] = src[g];
+      for (int g = g0 + lane % kLanes; g <= last; g += kLanes) dst[g - g0] = src[g];
     }
   }
 }
 
-// A persistent grid over sets of RT * 16 weight rows; 8 warps, each with its slice of k.
-template <class T, int RT, int NT, bool FEW, int GROUP, bool OFFSET>
-__global__ void __launch_bounds__(kW16Warps * 32, W16Shape<RT, NT, FEW, OFFSET>::kBlocks)
+// A persistent grid over sets of RT * 16 weight rows; each warp with its slice of k.
+template <class T, int RT, int NT, bool FEW, int WARPS, int GROUP, bool OFFSET>
+__global__ void __launch_bounds__(WARPS * 32, W16Shape<RT, NT, FEW, WARPS, OFFSET>::kBlocks)
     linear_w4a16_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const W16Args a) {
-  using Shape = W16Shape<RT, NT, FEW, OFFSET>;
+  using Shape = W16Shape<RT, NT, FEW, WARPS, OFFSET>;
   constexpr int kRows = Shape::kRows, kCols = Shape::kCols, kStages = Shape::kStages;
   constexpr int kGroups = kW16Cols / GROUP;            // groups of a stage
-  constexpr int kEvery = kW16Scales / kGroups;         // stages whose scales are held at a time
+  constexpr int kPitch = Shape::kPitch;
+  constexpr int kEvery = Shape::kHeld / kGroups;         // stages whose scales are held at a time
   extern __shared__ uint8_t smem_dyn[];
-  __shared__ uint64_t full[kW16Warps][kStages];
+  __shared__ uint64_t full[WARPS][kStages];
   uint8_t* smem = align1024_shared(smem_dyn);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int groups = a.K / GROUP;
   // this warp's stages of k
   const int units = (a.K + kW16Cols - 1) / kW16Cols;
-  const int u0 = units * warp / kW16Warps, n = units * (warp + 1) / kW16Warps - u0;
+  const int u0 = units * warp / WARPS, n = units * (warp + 1) / WARPS - u0;
   uint8_t* ring = smem + warp * kStages * Shape::kStage;
-  float* part = reinterpret_cast<float*>(smem + Shape::kRing);            // [2][warps][kRows][kCols]
-  uint16_t* scales = reinterpret_cast<uint16_t*>(smem + Shape::kRing + 2 * Shape::kPart + warp * Shape::kWarp);
-  const bool words = groups % 2 == 0 &&
-                     ((reinterpret_cast<uintptr_t>(a.scale) | reinterpret_cast<uintptr_t>(a.offset)) & 3) == 0;
+  float* part = reinterpret_cast<float*>(smem + Shape::kRing);            // [warps][kRows][kCols]
+  uint16_t* scales = reinterpret_cast<uint16_t*>(smem + Shape::kRing + Shape::kPart + warp * Shape::kWarp);
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(a.scale) | reinterpret_cast<uintptr_t>(a.offset);
+  const int unit = groups % 8 == 0 && (bits & 15) == 0 ? 8 : (groups % 2 == 0 && (bits & 3) == 0 ? 2 : 1);
 
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&full[warp][s], 1);
@@ -284,8 +289,8 @@ __global__ void __launch_bounds__(kW16Warps * 32, W16Shape<RT, NT, FEW, OFFSET>:
     if (sc_tile >= a.tiles || n == 0) return;
     const int first = (u0 + sc_i) * kGroups, count = min(kEvery, n - sc_i) * kGroups;
     uint16_t* to = scales + sc_b * (Shape::kScale / 2);
-    fetch_scales<kRows>(to, a.scale, sc_tile * kRows, a.N, groups, first, count, words);
-    if (OFFSET) fetch_scales<kRows>(to + Shape::kScale, a.offset, sc_tile * kRows, a.N, groups, first, count, words);
+    fetch_scales<kRows, kPitch>(to, a.scale, sc_tile * kRows, a.N, groups, first, count, unit);
+    if (OFFSET) fetch_scales<kRows, kPitch>(to + Shape::kScale, a.offset, sc_tile * kRows, a.N, groups, first, count, unit);
     sc_b ^= 1;
     sc_i += kEvery;
     if (sc_i >= n) sc_i = 0, sc_tile += gridDim.x;
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kW16Warps * 32, W16Shape<RT, NT, FEW, OFFSET>:
     for (int i = 0; i < kStages; ++i) issue();
   fetch();
 
-  int s = 0, buf = 0, sb = 0;
+  int s = 0, sb = 0;
   uint32_t phase = 0;
   bool ok = true;
   for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kW16Warps * 32, W16Shape<RT, NT, FEW, OFFSET>:
       if (i % kEvery == 0) {                           // this chunk has arrived, the next one sets off
         cp_async_wait();
         __syncwarp();
-        const int skip = ((u0 + i) * kGroups) & 1;
+        const int skip = ((u0 + i) * kGroups) & (unit - 1);
         sc = scales + sb * (Shape::kScale / 2) + skip;
         of = sc + Shape::kScale;
         sb ^= 1;
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(kW16Warps * 32, W16Shape<RT, NT, FEW, OFFSET>:
             for (int r = 0; r < RT; ++r)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int at = (16 * r + 8 * h + g) * kW16Pitch + e;
+                const int at = (16 * r + 8 * h + g) * kPitch + e;
                 const float sf = T::to_f32(sc[at]), o = OFFSET ? T::to_f32(of[at]) : 0.f;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
@@ -399,8 +404,9 @@ __global__ void __launch_bounds__(kW16Warps * 32, W16Shape<RT, NT, FEW, OFFSET>:
       if (++s == kStages) s = 0, phase ^= 1;
     }
 
-    // partial sums of the warps, joined in order; two buffers, so one barrier a tile
-    float* mine = part + (buf * kW16Warps + warp) * kRows * kCols;
+    // partial sums of the warps, joined in order
+    float* mine = part + warp * kRows * kCols;
+    if (tile != static_cast<int>(blockIdx.x)) __syncthreads();   // the last tile's sums have been read
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -412,17 +418,16 @@ __global__ void __launch_bounds__(kW16Warps * 32, W16Shape<RT, NT, FEW, OFFSET>:
                 make_float2(acc[r][j][2 * h], acc[r][j][2 * h + 1]);
     __syncthreads();
     // output i: row i % kRows, activation row i / kRows
-    for (int i = threadIdx.x; i < kRows * a.M; i += kW16Warps * 32) {
+    for (int i = threadIdx.x; i < kRows * a.M; i += WARPS * 32) {
       const int r = i % kRows, m = i / kRows, row = row0 + r;
-      const float* p = part + buf * kW16Warps * kRows * kCols + r * kCols + m;
+      const float* p = part + r * kCols + m;
       if (row < a.N) {
         float v = a.bias != nullptr ? T::to_f32(a.bias[row]) : 0.f;
 #pragma unroll
-        for (int w = 0; w < kW16Warps; ++w) v += p[w * kRows * kCols];
+        for (int w = 0; w < WARPS; ++w) v += p[w * kRows * kCols];
         a.y[m * a.ldy + row] = T::from_f32(v);
       }
     }
-    buf ^= 1;
   }
   if (!ok && lane == 0)                                // an expired wait: what is in flight lands before the CTA ends
     for (int i = 0; i < kStages; ++i) {
@@ -441,9 +446,9 @@ struct W16Call {
   cudaStream_t stream;
 };
 
-template <class T, int RT, int NT, bool FEW, int GROUP, bool OFFSET>
+template <class T, int RT, int NT, bool FEW, int WARPS, int GROUP, bool OFFSET>
 cudaError_t launch_w16(const W16Call& c, W16Args a) {
-  using Shape = W16Shape<RT, NT, FEW, OFFSET>;
+  using Shape = W16Shape<RT, NT, FEW, WARPS, OFFSET>;
   CUtensorMap tmW, tmX;
   if (tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.wq, a.N, a.K / 2, a.K / 2, 64, Shape::kRows,
                     CU_TENSOR_MAP_SWIZZLE_64B) != W4A4_OK ||
@@ -451,7 +456,7 @@ cudaError_t launch_w16(const W16Call& c, W16Args a) {
                     c.ldx * 2, FEW ? 128 : 64, a.M,
                     FEW ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) != W4A4_OK)
     return cudaErrorInvalidValue;
-  auto kernel = linear_w4a16_kernel<T, RT, NT, FEW, GROUP, OFFSET>;
+  auto kernel = linear_w4a16_kernel<T, RT, NT, FEW, WARPS, GROUP, OFFSET>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -468,7 +473,7 @@ cudaError_t launch_w16(const W16Call& c, W16Args a) {
   const int most = c.num_sms * Shape::kBlocks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.tiles < most ? a.tiles : most), 1, 1);
-  cfg.blockDim = dim3(kW16Warps * 32, 1, 1);
+  cfg.blockDim = dim3(WARPS * 32, 1, 1);
   cfg.dynamicSmemBytes = Shape::kSmem;
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[1];
@@ -482,11 +487,14 @@ cudaError_t launch_w16(const W16Call& c, W16Args a) {
 template <class T, int GROUP, bool OFFSET>
 cudaError_t launch_w16_rows(const W16Call& c, const W16Args& a) {
   if (a.M <= 2) {
-    if (a.N < 64 * c.num_sms) return launch_w16<T, 1, 1, true, GROUP, OFFSET>(c, a);
-    return launch_w16<T, 2, 1, true, GROUP, OFFSET>(c, a);
+    if (a.N < 64 * c.num_sms) return launch_w16<T, 1, 1, true, 8, GROUP, OFFSET>(c, a);
+    return launch_w16<T, 2, 1, true, 8, GROUP, OFFSET>(c, a);
   }
-  if (a.M <= 8) return launch_w16<T, 2, 1, false, GROUP, OFFSET>(c, a);
-  return launch_w16<T, 2, 2, false, GROUP, OFFSET>(c, a);
+  if (a.M <= 8) {
+    if (a.N < 64 * c.num_sms) return launch_w16<T, 2, 1, false, 16, GROUP, OFFSET>(c, a);
+    return launch_w16<T, 2, 1, false, 8, GROUP, OFFSET>(c, a);
+  }
+  return launch_w16<T, 2, 2, false, 12, GROUP, OFFSET>(c, a);
 }
 
 template <class T>
