@@ -57,6 +57,7 @@ namespace {
 constexpr int kTile = 128;             // query rows per MMA tile and keys per key tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kPoly = 2;               // of 16 pairs of weights, those taken by the polynomial
 constexpr float kRescale = 8.f;        // how far (log2) the maximum in use may fall behind
 
 struct AttnArgs {
@@ -164,7 +165,8 @@ struct AttnBars {
   uint64_t empty[SLOTS];
   uint64_t tail;           // the tile whose rows behind the sequence are zeroed
   uint64_t s_full[NQ];     // scores of the next tile are in tensor memory
-  uint64_t p_full[NQ];     // weights are in tensor memory (and O is rescaled)
+  uint64_t p_half[NQ];     // the first 64 keys' weights are in tensor memory (and O is rescaled)
+  uint64_t p_full[NQ];     // the other 64 keys' too
   uint64_t o_full[NQ];     // the last O += P V is done
   uint64_t drain;
   Place place;
@@ -184,6 +186,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
@@ -209,6 +217,41 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// 2^x of two numbers on the FMA and integer pipes, for x <= 128: x = j + f with j
+// whole and |f| <= 1/2, 2^f by a polynomial of degree 5 (least maximal
+// relative error on that interval, the constant term held at 1: 1.9e-7 with its
+// roundings), j added to the exponent.  Below -125 the result is 2^-125.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  const uint64_t v = pack2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  const uint64_t r = add2(v, pack2(12582912.f, 12582912.f));       // 1.5 2^23: the sum's low bits are j
+  const uint64_t j = add2(r, pack2(-12582912.f, -12582912.f));
+  const uint64_t f = fma2(j, pack2(-1.f, -1.f), v);
+  uint64_t p = pack2(0.001326472731307149f, 0.001326472731307149f);
+  p = fma2(p, f, pack2(0.009671512991189957f, 0.009671512991189957f));
+  p = fma2(p, f, pack2(0.05550733581185341f, 0.05550733581185341f));
+  p = fma2(p, f, pack2(0.24022242426872253f, 0.24022242426872253f));
+  p = fma2(p, f, pack2(0.6931470036506653f, 0.6931470036506653f));
+  p = fma2(p, f, pack2(1.f, 1.f));
+  const float2 q = unpack2(p), n = unpack2(r);
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
+                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
+}
+
+// The weights 2^(c s + shift) of 32 scores, in place and as 16 pairs of 16
+// bits.  POLY of every 16 pairs take the polynomial, so that the exponential
+// unit (four lanes a cycle and quarter of an SM) and the FMA pipe share them.
+template <class T, int POLY>
+__device__ __forceinline__ void weigh32(uint32_t (&s)[32], uint64_t cc, uint64_t ss, uint32_t (&p)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 x = unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cc, ss));
+    const float2 w = i * POLY % 16 < POLY ? ex2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
+    s[2 * i] = __float_as_uint(w.x);
+    s[2 * i + 1] = __float_as_uint(w.y);
+    p[i] = T::from_f32x2(w.x, w.y);
+  }
 }
 
 template <class T, int D, int NQ, bool SPLIT>
@@ -239,6 +282,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
       mbar_init(&bars.tail, 1);
       for (int t = 0; t < NQ; ++t) {
         mbar_init(&bars.s_full[t], 1);
+        mbar_init(&bars.p_half[t], 4);
         mbar_init(&bars.p_full[t], 4);
         mbar_init(&bars.o_full[t], 1);
       }
@@ -389,13 +433,17 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
 #pragma unroll
           for (int t = 0; t < NQ; ++t) {
             if (!ok || j >= n[t]) continue;
-            ok = mbar_wait(&bars.p_full[t], j & 1, abort_flag, a.status, a.wait_ns);
-            if (!ok) continue;
-            tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_f16_ts(tmem_base + Shape::o_col(t), tmem_base + Shape::s_col(t) + k * 8,
-                         vd + sv * (Shape::kSlot >> 4) + k * (16 * 128 >> 4), idesc_o, (j | k) != 0 ? 1u : 0u);
+            for (int half = 0; half < 2; ++half) {
+              ok = mbar_wait(half == 0 ? &bars.p_half[t] : &bars.p_full[t], j & 1, abort_flag, a.status, a.wait_ns);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = half * (kTile / 32); k < (half + 1) * (kTile / 32); ++k)
+                mma_f16_ts(tmem_base + Shape::o_col(t), tmem_base + Shape::s_col(t) + k * 8,
+                           vd + sv * (Shape::kSlot >> 4) + k * (16 * 128 >> 4), idesc_o, (j | k) != 0 ? 1u : 0u);
+            }
+            if (!ok) continue;
             if (j + 1 == n[t]) mma_commit(&bars.o_full[t]);
             // the last reader of this v tile frees its slot
             if (t == NQ - 1 || j >= n[NQ - 1]) mma_commit(&bars.empty[sv]);
@@ -446,7 +494,8 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
 #pragma unroll
         for (int g = 0; g < 4; ++g) tmem_ld_32x32b_x32(s_at + 32 * g, sv[g]);
         tmem_wait_ld();
-        if (fewest < (j + 1) * kTile) {              // a tile that a mask cuts (the same for the warp)
+        const bool cut = fewest < (j + 1) * kTile;   // a tile that a mask cuts (the same for the warp)
+        if (cut) {
           const int lim = seen - j * kTile;
 #pragma unroll
           for (int g = 0; g < 4; ++g)
@@ -458,10 +507,10 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
         for (int g = 0; g < 4; ++g) {
           mx[g] = __uint_as_float(sv[g][0]);
 #pragma unroll
-          for (int i = 1; i < 31; i += 2) mx[g] = fmaxf(fmaxf(mx[g], __uint_as_float(sv[g][i])), __uint_as_float(sv[g][i + 1]));
-          mx[g] = fmaxf(mx[g], __uint_as_float(sv[g][31]));
+          for (int i = 1; i < 31; i += 2) mx[g] = max3(mx[g], __uint_as_float(sv[g][i]), __uint_as_float(sv[g][i + 1]));
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], __uint_as_float(sv[0][31]), __uint_as_float(sv[1][31])),
+                               max3(__uint_as_float(sv[2][31]), __uint_as_float(sv[3][31]), -INFINITY)) * c;
         const bool behind = top - m > kRescale;      // false for -inf - -inf
         if (j == 0) {
           if (behind) m = top;
@@ -482,26 +531,23 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
             tmem_st_32x32b_x16(o_at + 16 * g, o);
           }
         }
-        const float shift = m == -INFINITY ? 0.f : -m;
+        // a NaN score makes the whole row NaN (the polynomial would lose it)
+        const float shift = top != top ? top : (m == -INFINITY ? 0.f : -m);
         const uint64_t cc = pack2(c, c), ss = pack2(shift, shift);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint32_t* e = &sv[g][2 * i];
-            const float2 x = unpack2(fma2(pack2(__uint_as_float(e[0]), __uint_as_float(e[1])), cc, ss));
-            const float p0 = ex2(x.x), p1 = ex2(x.y);
-            e[0] = __float_as_uint(p0);
-            e[1] = __float_as_uint(p1);
-            p[i] = T::from_f32x2(p0, p1);
-          }
+          // where a mask cuts, -inf has to give exactly 0
+          if (cut) weigh32<T, 0>(sv[g], cc, ss, p);
+          else weigh32<T, kPoly>(sv[g], cc, ss, p);
           tmem_st_32x32b_x16(s_at + 16 * g, p);
+          if (g & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(g == 1 ? &bars.p_half[t] : &bars.p_full[t]);
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[t]);
         // the sum, off the path of the MMA
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
