@@ -137,6 +137,38 @@ def test_long_prompt(cuda_lib, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,Hq,Hk", [
+    ([1100], 40, 40),                       # two query tiles per block: more blocks than the GPU has SMs
+    ([1025, 130, 1, 257, 0, 700], 40, 8),   # groups of five: 125 rows of a tile
+    ([900, 300, 515], 48, 6),
+])
+def test_more_blocks_than_sms(cuda_lib, dtype, causal, D, n, Hq, Hk):
+    go(n, n, Hq, Hk, D, dtype, causal, seed=Hq)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_blocks_than_sms_edges(cuda_lib, D):
+    """The same kernel with what its last tiles must not read (NaN behind every
+    sequence), queries that see nothing, sharp scores and keys that fall and rise."""
+    qs, ks, Hq, Hk = [700, 900, 520], [650, 1200, 0], 32, 8
+    go(qs, ks, Hq, Hk, D, torch.bfloat16, True, spread=4.0)
+    q, k, v = make(sum(qs), sum(ks), Hq, Hk, D, torch.bfloat16)
+    k *= torch.linspace(-6.0, 6.0, sum(ks), device="cuda")[:, None, None].to(k.dtype)
+    out, lse = w4.attention(q, k, v, cu(qs), cu(ks), causal=True, return_lse=True)
+    check(out, lse, q, k, v, qs, ks, True)
+    bad = lambda t: torch.cat((t, torch.full((200, *t.shape[1:]), math.nan, device="cuda", dtype=t.dtype)))
+    again = w4.attention(bad(q), bad(k), bad(v), cu(qs), cu(ks), causal=True)
+    assert torch.equal(again[:sum(qs)], out)
+    k[:650], v[:650] = math.nan, math.nan
+    again = w4.attention(q, k, v, cu(qs), cu(ks), causal=True)
+    assert torch.equal(again[700:], out[700:]) and torch.isnan(again[100:700]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("spread,scale", [(8.0, None), (0.01, None), (1.0, 1.0), (1.0, 1e-6), (3.0, 0.5)])
 def test_sharp_and_flat_softmax(cuda_lib, spread, scale):
     """Scores of hundreds, where the running maximum moves by much from tile to

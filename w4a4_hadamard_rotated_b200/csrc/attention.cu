@@ -57,7 +57,6 @@ namespace {
 constexpr int kTile = 128;             // query rows per MMA tile and keys per key tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kPoly = 2;               // of 16 pairs of weights, those taken by the polynomial
 constexpr float kRescale = 8.f;        // how far (log2) the maximum in use may fall behind
 
 struct AttnArgs {
@@ -175,11 +174,61 @@ struct AttnBars {
   int abort_flag;
 };
 
-// Wait by every lane of the warp; one verdict for all of them.
+// Wait by a whole warp, which stays converged: every lane tries, one verdict
+// for all.  The clock and the abort flag are looked at every 32nd try.  (Lane 0
+// polling for the others costs more: 503 against 408 us on the packed prompts.)
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status,
                                          unsigned long long wait_ns) {
-  const bool ok = mbar_wait(bar, parity, abort, status, wait_ns);
-  return __all_sync(0xFFFFFFFFu, ok);
+  const uint32_t at = smem_u32(bar);
+  if (__all_sync(0xFFFFFFFFu, mbar_test(at, parity))) return true;
+  const unsigned long long t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (__all_sync(0xFFFFFFFFu, mbar_test(at, parity))) return true;
+    const bool late = global_ns() - t0 > wait_ns;
+    if (late) {
+      if (status != nullptr) atomicOr(status, 8u /* W4A4_ERR_TIMEOUT */);
+      if (abort != nullptr) *abort = 1;
+    }
+    if (__any_sync(0xFFFFFFFFu, late || (abort != nullptr && *abort))) return false;
+  }
+}
+
+// MMA issue by a whole warp, `elected` in one lane: the operands' addresses
+// stay in uniform registers, which code under a lane's branch cannot use (a
+// measured 75 cycles an instruction there, against the 64 it runs).  The
+// descriptors' upper halves are constants.
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) {
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(elected)
+      : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -219,38 +268,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 2^x of two numbers on the FMA and integer pipes, for x <= 128: x = j + f with j
-// whole and |f| <= 1/2, 2^f by a polynomial of degree 5 (least maximal
-// relative error on that interval, the constant term held at 1: 1.9e-7 with its
-// roundings), j added to the exponent.  Below -125 the result is 2^-125.
-__device__ __forceinline__ float2 ex2_poly(float2 x) {
-  const uint64_t v = pack2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
-  const uint64_t r = add2(v, pack2(12582912.f, 12582912.f));       // 1.5 2^23: the sum's low bits are j
-  const uint64_t j = add2(r, pack2(-12582912.f, -12582912.f));
-  const uint64_t f = fma2(j, pack2(-1.f, -1.f), v);
-  uint64_t p = pack2(0.001326472731307149f, 0.001326472731307149f);
-  p = fma2(p, f, pack2(0.009671512991189957f, 0.009671512991189957f));
-  p = fma2(p, f, pack2(0.05550733581185341f, 0.05550733581185341f));
-  p = fma2(p, f, pack2(0.24022242426872253f, 0.24022242426872253f));
-  p = fma2(p, f, pack2(0.6931470036506653f, 0.6931470036506653f));
-  p = fma2(p, f, pack2(1.f, 1.f));
-  const float2 q = unpack2(p), n = unpack2(r);
-  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
-                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
-}
-
-// The weights 2^(c s + shift) of 32 scores, in place and as 16 pairs of 16
-// bits.  POLY of every 16 pairs take the polynomial, so that the exponential
-// unit (four lanes a cycle and quarter of an SM) and the FMA pipe share them.
-template <class T, int POLY>
+// The weights 2^(c s + shift) of 32 scores, in place and as 16 pairs of 16 bits.
+// (A polynomial on the FMA pipe for an eighth or a quarter of them, to relieve
+// the exponential unit, measured slower: 5.29 and 5.42 against 5.15 ms at
+// 32760 keys x 10 heads, where the power cap binds.)
+template <class T>
 __device__ __forceinline__ void weigh32(uint32_t (&s)[32], uint64_t cc, uint64_t ss, uint32_t (&p)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float2 x = unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cc, ss));
-    const float2 w = i * POLY % 16 < POLY ? ex2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
-    s[2 * i] = __float_as_uint(w.x);
-    s[2 * i + 1] = __float_as_uint(w.y);
-    p[i] = T::from_f32x2(w.x, w.y);
+    const float w0 = ex2(x.x), w1 = ex2(x.y);
+    s[2 * i] = __float_as_uint(w0);
+    s[2 * i + 1] = __float_as_uint(w1);
+    p[i] = T::from_f32x2(w0, w1);
   }
 }
 
@@ -401,66 +431,81 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0 && n_all > 0) {
+      if (n_all > 0) {
         constexpr uint32_t idesc_s = idesc_f16(kTile, kTile, kBf16, false);
         constexpr uint32_t idesc_o = idesc_f16(kTile, D, kBf16, true);
+        const uint32_t el = lane == 0 ? 1u : 0u;
         const uint64_t qd = sw128_kmajor_desc(smem_u32(smem));
         const uint64_t kd = sw128_kmajor_desc(smem_u32(ring));
         const uint64_t vd = sw128_mnmajor_desc(smem_u32(ring), Shape::kBox);
-        auto score = [&](int t, int slot) {
+        const uint32_t q_lo = static_cast<uint32_t>(qd), k_lo = static_cast<uint32_t>(kd), v_lo = static_cast<uint32_t>(vd);
+        const uint32_t k_hi = static_cast<uint32_t>(kd >> 32), v_hi = static_cast<uint32_t>(vd >> 32);
+        auto score = [&](int t, uint32_t kt) {         // kt: the k tile's descriptor, lower half
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t step = (k / 4) * (Shape::kBox >> 4) + (k % 4) * 2;
-            mma_bf16(tmem_base + Shape::s_col(t), qd + t * (Shape::kChunks * Shape::kBox >> 4) + step,
-                     kd + slot * (Shape::kSlot >> 4) + step, idesc_s, k != 0 ? 1u : 0u);
+            const uint64_t qa = desc64(q_lo + t * (Shape::kChunks * Shape::kBox >> 4) + step, k_hi);
+            const uint64_t ka = desc64(kt + step, k_hi);
+            if (k == 0) mma_ss<false>(el, tmem_base + Shape::s_col(t), qa, ka, idesc_s);
+            else mma_ss<true>(el, tmem_base + Shape::s_col(t), qa, ka, idesc_s);
           }
-          mma_commit(&bars.s_full[t]);
+          commit(el, &bars.s_full[t]);
         };
-        bool ok = mbar_wait(&bars.q_full, 0, abort_flag, a.status, a.wait_ns) &&
-                  mbar_wait(&bars.full[0], 0, abort_flag, a.status, a.wait_ns);
+        bool ok = wait_all(&bars.q_full, 0, abort_flag, a.status, a.wait_ns) &&
+                  wait_all(&bars.full[0], 0, abort_flag, a.status, a.wait_ns);
         if (ok) {
           tc_fence_after();
 #pragma unroll
           for (int t = 0; t < NQ; ++t)
-            if (n[t] > 0) score(t, 0);
-          mma_commit(&bars.empty[0]);
+            if (n[t] > 0) score(t, k_lo);
+          commit(el, &bars.empty[0]);
         }
+        int slot = 0;                                  // of the k tile last used
+        uint32_t phase = 0;
+        auto next = [&] {
+          if (++slot == kSlots) slot = 0, phase ^= 1;
+        };
         for (int j = 0; ok && j < n_all; ++j) {
-          const int iv = 2 * j + 1, ik = 2 * j + 2;
-          const int sv = iv % kSlots, sk = ik % kSlots;
-          ok = mbar_wait(&bars.full[sv], (iv / kSlots) & 1, abort_flag, a.status, a.wait_ns);
+          next();
+          const int sv = slot;
+          ok = wait_all(&bars.full[sv], phase, abort_flag, a.status, a.wait_ns);
+          next();
+          const int sk = slot;
+          const uint32_t vt = v_lo + sv * (Shape::kSlot >> 4), kt = k_lo + sk * (Shape::kSlot >> 4);
           bool k_ready = false;
 #pragma unroll
           for (int t = 0; t < NQ; ++t) {
             if (!ok || j >= n[t]) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              ok = mbar_wait(half == 0 ? &bars.p_half[t] : &bars.p_full[t], j & 1, abort_flag, a.status, a.wait_ns);
+              ok = ok && wait_all(half == 0 ? &bars.p_half[t] : &bars.p_full[t], j & 1, abort_flag, a.status, a.wait_ns);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
               for (int k = half * (kTile / 32); k < (half + 1) * (kTile / 32); ++k)
-                mma_f16_ts(tmem_base + Shape::o_col(t), tmem_base + Shape::s_col(t) + k * 8,
-                           vd + sv * (Shape::kSlot >> 4) + k * (16 * 128 >> 4), idesc_o, (j | k) != 0 ? 1u : 0u);
+                mma_ts(el, tmem_base + Shape::o_col(t), tmem_base + Shape::s_col(t) + k * 8,
+                       desc64(vt + k * (16 * 128 >> 4), v_hi), idesc_o, k != 0 ? 1u : (j != 0 ? 1u : 0u));
             }
             if (!ok) continue;
-            if (j + 1 == n[t]) mma_commit(&bars.o_full[t]);
-            // the last reader of this v tile frees its slot
-            if (t == NQ - 1 || j >= n[NQ - 1]) mma_commit(&bars.empty[sv]);
+            if (j + 1 == n[t]) commit(el, &bars.o_full[t]);
             if (j + 1 < n[t]) {
               if (!k_ready) {
-                ok = mbar_wait(&bars.full[sk], (ik / kSlots) & 1, abort_flag, a.status, a.wait_ns);
+                ok = wait_all(&bars.full[sk], phase, abort_flag, a.status, a.wait_ns);
                 if (!ok) continue;
                 tc_fence_after();
                 k_ready = true;
               }
-              score(t, sk);
+              score(t, kt);
             }
           }
-          if (ok && j + 1 < n_all) mma_commit(&bars.empty[sk]);
+          // the tiles' last readers free the slots
+          if (ok) {
+            commit(el, &bars.empty[sv]);
+            if (j + 1 < n_all) commit(el, &bars.empty[sk]);
+          }
         }
-        mma_commit(&bars.drain);
-        (void)mbar_wait(&bars.drain, 0, nullptr, nullptr, 100000000ull);
+        commit(el, &bars.drain);
+        if (lane == 0) (void)mbar_wait(&bars.drain, 0, nullptr, nullptr, 100000000ull);
       }
       __syncwarp();
     } else {
@@ -494,8 +539,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
 #pragma unroll
         for (int g = 0; g < 4; ++g) tmem_ld_32x32b_x32(s_at + 32 * g, sv[g]);
         tmem_wait_ld();
-        const bool cut = fewest < (j + 1) * kTile;   // a tile that a mask cuts (the same for the warp)
-        if (cut) {
+        if (fewest < (j + 1) * kTile) {              // a tile that a mask cuts (the same for the warp)
           const int lim = seen - j * kTile;
 #pragma unroll
           for (int g = 0; g < 4; ++g)
@@ -531,15 +575,12 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
             tmem_st_32x32b_x16(o_at + 16 * g, o);
           }
         }
-        // a NaN score makes the whole row NaN (the polynomial would lose it)
-        const float shift = top != top ? top : (m == -INFINITY ? 0.f : -m);
+        const float shift = m == -INFINITY ? 0.f : -m;
         const uint64_t cc = pack2(c, c), ss = pack2(shift, shift);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t p[16];
-          // where a mask cuts, -inf has to give exactly 0
-          if (cut) weigh32<T, 0>(sv[g], cc, ss, p);
-          else weigh32<T, kPoly>(sv[g], cc, ss, p);
+          weigh32<T>(sv[g], cc, ss, p);
           tmem_st_32x32b_x16(s_at + 16 * g, p);
           if (g & 1) {
             tmem_wait_st();
@@ -683,9 +724,9 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
   p.blocks = p.nq == 1 ? Tq / p.tokens + B : Tq / (2 * p.tokens) + B;
   p.chunks = 1;
   if (p.nq == 1 && one < 296) {
-    // about three rounds of two blocks per SM, chunks of four key tiles at least
+    // about two rounds of two blocks per SM, chunks of four key tiles at least
     const int64_t tiles = (Tk + kTile - 1) / kTile;
-    int64_t chunk = (tiles * one + B * 888 - 1) / (B * 888);
+    int64_t chunk = (tiles * one + B * 592 - 1) / (B * 592);
     if (chunk < 4) chunk = 4;
     if (chunk * B < tiles) {
       p.chunk = static_cast<int>(chunk);
