@@ -174,27 +174,6 @@ struct AttnBars {
   int abort_flag;
 };
 
-// Wait by a whole warp, which stays converged: every lane tries, one verdict
-// for all.  The clock and the abort flag are looked at every 32nd try.  (Lane 0
-// polling for the others costs more: 503 against 408 us on the packed prompts.)
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status,
-                                         unsigned long long wait_ns) {
-  const uint32_t at = smem_u32(bar);
-  if (__all_sync(0xFFFFFFFFu, mbar_test(at, parity))) return true;
-  const unsigned long long t0 = global_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (__all_sync(0xFFFFFFFFu, mbar_test(at, parity))) return true;
-    const bool late = global_ns() - t0 > wait_ns;
-    if (late) {
-      if (status != nullptr) atomicOr(status, 8u /* W4A4_ERR_TIMEOUT */);
-      if (abort != nullptr) *abort = 1;
-    }
-    if (__any_sync(0xFFFFFFFFu, late || (abort != nullptr && *abort))) return false;
-  }
-}
-
 // MMA issue by a whole warp, `elected` in one lane: the operands' addresses
 // stay in uniform registers, which code under a lane's branch cannot use (a
 // measured 75 cycles an instruction there, against the 64 it runs).  The
@@ -387,7 +366,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
         bool tail_pending = false;
         for (int i = 0; i < 2 * n_all; ++i) {
           const int s = i % kSlots;
-          if (!wait_all(&bars.empty[s], ((i / kSlots) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) break;
+          if (!warp_wait_converged(&bars.empty[s], ((i / kSlots) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) break;
           const int row = (j0 + i / 2) * kTile;                 // first key of the tile, within the sequence
           const bool is_v = (i & 1) != 0;
           // value rows behind the sequence that are rows of the tensor (the
@@ -403,7 +382,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
           ++issued;
           if (cut) {   // at most once: the sequence's last tile
             // the wait ignores the abort flag: the copy always lands
-            tail_pending = !wait_all(&bars.tail, 0, nullptr, a.status, a.wait_ns);
+            tail_pending = !warp_wait_converged(&bars.tail, 0, nullptr, a.status, a.wait_ns);
             if (tail_pending) {
               *abort_flag = 1;
               break;
@@ -451,8 +430,8 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
           }
           commit(el, &bars.s_full[t]);
         };
-        bool ok = wait_all(&bars.q_full, 0, abort_flag, a.status, a.wait_ns) &&
-                  wait_all(&bars.full[0], 0, abort_flag, a.status, a.wait_ns);
+        bool ok = warp_wait_converged(&bars.q_full, 0, abort_flag, a.status, a.wait_ns) &&
+                  warp_wait_converged(&bars.full[0], 0, abort_flag, a.status, a.wait_ns);
         if (ok) {
           tc_fence_after();
 #pragma unroll
@@ -468,7 +447,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
         for (int j = 0; ok && j < n_all; ++j) {
           next();
           const int sv = slot;
-          ok = wait_all(&bars.full[sv], phase, abort_flag, a.status, a.wait_ns);
+          ok = warp_wait_converged(&bars.full[sv], phase, abort_flag, a.status, a.wait_ns);
           next();
           const int sk = slot;
           const uint32_t vt = v_lo + sv * (Shape::kSlot >> 4), kt = k_lo + sk * (Shape::kSlot >> 4);
@@ -478,7 +457,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
             if (!ok || j >= n[t]) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              ok = ok && wait_all(half == 0 ? &bars.p_half[t] : &bars.p_full[t], j & 1, abort_flag, a.status, a.wait_ns);
+              ok = ok && warp_wait_converged(half == 0 ? &bars.p_half[t] : &bars.p_full[t], j & 1, abort_flag, a.status, a.wait_ns);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
@@ -490,7 +469,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
             if (j + 1 == n[t]) commit(el, &bars.o_full[t]);
             if (j + 1 < n[t]) {
               if (!k_ready) {
-                ok = wait_all(&bars.full[sk], phase, abort_flag, a.status, a.wait_ns);
+                ok = warp_wait_converged(&bars.full[sk], phase, abort_flag, a.status, a.wait_ns);
                 if (!ok) continue;
                 tc_fence_after();
                 k_ready = true;
@@ -532,7 +511,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
       const float c = a.scale_log2;
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
-        ok = wait_all(&bars.s_full[t], j & 1, abort_flag, a.status, a.wait_ns);
+        ok = warp_wait_converged(&bars.s_full[t], j & 1, abort_flag, a.status, a.wait_ns);
         if (!ok) break;
         tc_fence_after();
         uint32_t sv[4][32];
@@ -598,7 +577,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
         }
       }
       if (ok && nt > 0) {
-        ok = wait_all(&bars.o_full[t], 0, abort_flag, a.status, a.wait_ns);
+        ok = warp_wait_converged(&bars.o_full[t], 0, abort_flag, a.status, a.wait_ns);
         tc_fence_after();
       }
       if (ok) {

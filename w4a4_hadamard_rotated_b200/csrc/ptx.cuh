@@ -178,6 +178,30 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
 }
 
+// Warp-wide wait that keeps the warp converged: every lane tries, one vote is
+// the verdict, and the clock and the abort flag are looked at every 32nd round
+// only.  Where a warp's next instructions use the whole warp and the wait is
+// on the critical path it beats lane 0 polling for the others (attention over
+// packed prompts: 375 against 503 us) and each lane polling by itself (408).
+__device__ __forceinline__ bool warp_wait_converged(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                    unsigned int* status,
+                                                    unsigned long long limit_ns = kWaitLimitNs) {
+  const uint32_t at = smem_u32(bar);
+  if (__all_sync(0xFFFFFFFFu, mbar_test(at, parity))) return true;
+  const unsigned long long t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (__all_sync(0xFFFFFFFFu, mbar_test(at, parity))) return true;
+    const bool late = global_ns() - t0 > limit_ns;
+    if (late) {
+      if (status != nullptr) atomicOr(status, 8u /* W4A4_ERR_TIMEOUT */);
+      if (abort != nullptr) *abort = 1;
+    }
+    if (__any_sync(0xFFFFFFFFu, late || (abort != nullptr && *abort))) return false;
+  }
+}
+
 // Named barrier `id` over `nthreads` threads (a multiple of 32) that also
 // ORs `pred` across them: every participating thread gets the same answer,
 // so warps that branch on it (e.g. on an abort flag another thread may raise

@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(WARPS * 32, W16Shape<RT, NT, FEW, WARPS, OFFSE
         sb ^= 1;
         fetch();
       }
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[warp][s], phase, nullptr, a.status, a.wait_ns));
+      ok = warp_wait_converged(&full[warp][s], phase, nullptr, a.status, a.wait_ns);
       if (!ok) break;
       const uint32_t wbase = smem_u32(ring + s * Shape::kStage), xbase = wbase + Shape::kW;
       float sum[RT][NT][4], xs[NT][4];
