@@ -476,17 +476,25 @@ def rotary_frequencies(axis_dims, theta=10000.0, device="cuda"):
             torch.tensor(axis, dtype=torch.int32, device=device))
 
 
-def _heads(t, name, T, H, D, dtype, index):
+def _heads(t, name, shape, dtype, index):
     """(address, token stride, head stride) of a [T, H, D] tensor with
     contiguous D; a dimension of one or no element has no stride of its own."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype} on cuda:{index}")
-    if t.shape != (T, H, D):
-        raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    T, H, D = shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * D, D
     st, sh, sd = t.stride()
-    if sd != 1 and t.numel():
+    if sd != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
     return t.data_ptr(), st if T > 1 else H * D, sh if H > 1 else D
+
+
+def _new_like(t):
+    """A contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _positions(positions, freq, axis, T, index):
@@ -528,24 +536,28 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, freq=N
     code = _need_16bit(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D]")
-    T, Hq, D = q.shape
+    shape = q.shape
+    T, Hq, D = shape
     index, dtype = q.get_device(), q.dtype
-    qp, qt, qh = _heads(q, "q", T, Hq, D, dtype, index)
+    qp, qt, qh = _heads(q, "q", shape, dtype, index)
     if q_out is None:
-        q_out = q.new_empty((T, Hq, D))
+        q_out = _new_like(q)
         qo = (q_out.data_ptr(), Hq * D, D)
     else:
-        qo = _heads(q_out, "q_out", T, Hq, D, dtype, index)
+        qo = _heads(q_out, "q_out", shape, dtype, index)
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 3:
             raise ValueError("k must be [T, Hk, D]")
-        Hk = k.shape[1]
-        kp, kt, kh = _heads(k, "k", T, Hk, D, dtype, index)
+        shape = k.shape
+        Hk = shape[1]
+        if shape[0] != T or shape[2] != D:
+            raise ValueError(f"k must be [{T}, Hk, {D}], got {list(shape)}")
+        kp, kt, kh = _heads(k, "k", shape, dtype, index)
         if k_out is None:
-            k_out = k.new_empty((T, Hk, D))
+            k_out = _new_like(k)
             ko = (k_out.data_ptr(), Hk * D, D)
         else:
-            ko = _heads(k_out, "k_out", T, Hk, D, dtype, index)
+            ko = _heads(k_out, "k_out", shape, dtype, index)
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
     else:
@@ -574,17 +586,20 @@ def attention(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, causal=False, scale
     code = _need_16bit(q, "q")
     if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("q must be [Tq, Hq, D] and k, v [Tk, Hk, D]")
-    Tq, Hq, D = q.shape
-    Tk, Hk, _ = k.shape
+    qshape, kshape = q.shape, k.shape
+    Tq, Hq, D = qshape
+    Tk, Hk, Dk = kshape
+    if Dk != D:
+        raise ValueError(f"q and k must have the same last dimension, got {D} and {Dk}")
     index, dtype = q.get_device(), q.dtype
-    qs = _heads(q, "q", Tq, Hq, D, dtype, index)
-    ks = _heads(k, "k", Tk, Hk, D, dtype, index)
-    vs = _heads(v, "v", Tk, Hk, D, dtype, index)
+    qs = _heads(q, "q", qshape, dtype, index)
+    ks = _heads(k, "k", kshape, dtype, index)
+    vs = _heads(v, "v", kshape, dtype, index)
     if out is None:
-        out = q.new_empty((Tq, Hq, D))
+        out = _new_like(q)
         os_ = (out.data_ptr(), Hq * D, D)
     else:
-        os_ = _heads(out, "out", Tq, Hq, D, dtype, index)
+        os_ = _heads(out, "out", qshape, dtype, index)
     B, cq, ck = 1, None, None
     if cu_seqlens_q is not None or cu_seqlens_k is not None:
         if cu_seqlens_q is None or cu_seqlens_k is None:
