@@ -176,6 +176,7 @@ struct W16Args {
 // FEW: one or two activation rows.  WARPS: of a CTA, which share k.
 template <int RT, int NT, bool FEW, int WARPS, bool OFFSET>
 struct W16Shape {
+  static_assert(RT == 1 || RT == 2, "rows of a warp: whole lanes' worth of scales");
   static constexpr int kRows = RT * 16;
   static constexpr int kCols = FEW ? 2 : NT * 8;             // columns of a partial sum
   static constexpr uint32_t kW = kRows * 64;                 // codes of a stage
@@ -184,7 +185,7 @@ struct W16Shape {
   static constexpr uint32_t kXBox = FEW ? 512 : NT * 1024;
   static constexpr uint32_t kX = FEW ? 512 : 2 * kXBox;
   static constexpr uint32_t kStage = kW + kX;          // a multiple of the swizzles' period: 512 bytes, with x swizzled 1024
-  static constexpr int kStages = FEW ? 3 : 2;
+  static constexpr int kStages = FEW && WARPS <= 8 ? 3 : 2;
   // groups of a row whose scales a warp holds at a time (with offsets, which
   // take as much room again, half as many), and the row pitch that holds them
   // from any beginning, rounded down to 8 groups
@@ -304,6 +305,9 @@ __global__ void __launch_bounds__(WARPS * 32, W16Shape<RT, NT, FEW, WARPS, OFFSE
   bool ok = true;
   for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
     const int row0 = tile * kRows;
+    // the row this thread writes in the end (the threads are whole multiples of kRows)
+    const int r_out = threadIdx.x % kRows, row = row0 + r_out;
+    const float bias = a.bias != nullptr && row < a.N ? T::to_f32(a.bias[row]) : 0.f;
     float acc[RT][NT][4] = {};
     const uint16_t *sc = scales, *of = scales;
     for (int i = 0; i < n && ok; ++i) {
@@ -417,12 +421,10 @@ __global__ void __launch_bounds__(WARPS * 32, W16Shape<RT, NT, FEW, WARPS, OFFSE
             *reinterpret_cast<float2*>(&mine[(16 * r + 8 * h + g) * kCols + 8 * j + 2 * t]) =
                 make_float2(acc[r][j][2 * h], acc[r][j][2 * h + 1]);
     __syncthreads();
-    // output i: row i % kRows, activation row i / kRows
-    for (int i = threadIdx.x; i < kRows * a.M; i += WARPS * 32) {
-      const int r = i % kRows, m = i / kRows, row = row0 + r;
-      const float* p = part + r * kCols + m;
+    for (int m = threadIdx.x / kRows; m < a.M; m += WARPS * 32 / kRows) {
+      const float* p = part + r_out * kCols + m;
       if (row < a.N) {
-        float v = a.bias != nullptr ? T::to_f32(a.bias[row]) : 0.f;
+        float v = bias;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) v += p[w * kRows * kCols];
         a.y[m * a.ldy + row] = T::from_f32(v);
