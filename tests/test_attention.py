@@ -352,3 +352,22 @@ def test_binding_refusals(cuda_lib):
     for kind, call in bad:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.gpu
+def test_expired_waits_end_the_call(cuda_lib):
+    """With a wait limit of a few nanoseconds the kernels give up, report it and
+    leave the context as it was; the next call is right."""
+    cases = [make(1100, 1100, 40, 40, 128, torch.bfloat16), make(300, 300, 4, 4, 64, torch.float16),
+             make(1, 9000, 8, 2, 128, torch.bfloat16)]
+    good = [w4.attention(*c, causal=True) for c in cases]
+    w4.debug_set_wait_limit(5)
+    try:
+        for c in cases:
+            w4.attention(*c, causal=True)
+            assert w4.last_device_error() == 8
+    finally:
+        w4.debug_set_wait_limit(0)
+    for c, g in zip(cases, good):
+        assert torch.equal(w4.attention(*c, causal=True), g)
+    assert w4.last_device_error() == 0

@@ -217,3 +217,24 @@ def test_binding_refusals(cuda_lib):
     for kind, call in bad:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.gpu
+def test_expired_waits_end_the_call(cuda_lib):
+    """With a wait limit of a few nanoseconds the kernel gives up a wait that it
+    has to wait for (data may be there already), reports it and leaves the
+    context as it was; the next call is right."""
+    cases = [on_gpu(*make(M, 5120, 4000, 64, torch.bfloat16, True, False)) for M in (1, 5, 16)]
+    good = [w4.linear_w4a16(x, c, s, offset=o) for x, c, s, o, _ in cases]
+    w4.debug_set_wait_limit(5)
+    seen = set()
+    try:
+        for x, c, s, o, _ in cases * 5:
+            w4.linear_w4a16(x, c, s, offset=o)
+            seen.add(w4.last_device_error())
+    finally:
+        w4.debug_set_wait_limit(0)
+    assert seen <= {0, 8}
+    for (x, c, s, o, _), g in zip(cases, good):
+        assert torch.equal(w4.linear_w4a16(x, c, s, offset=o), g)
+    assert w4.last_device_error() == 0

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
           }
           commit(el, &bars.s_full[t]);
         };
-        bool ok = warp_wait_converged(&bars.q_full, 0, abort_flag, a.status, a.wait_ns) &&
+        bool ok = warp_wait_converged<true>(&bars.q_full, 0, abort_flag, a.status, a.wait_ns) &&
                   warp_wait_converged(&bars.full[0], 0, abort_flag, a.status, a.wait_ns);
         if (ok) {
           tc_fence_after();

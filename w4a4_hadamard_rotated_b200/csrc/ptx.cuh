@@ -75,6 +75,19 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without suspending the thread.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait until the phase with the given parity has completed.  Gives up after
 // limit_ns (or at once when *abort is set by another thread of the CTA),
 // ORs W4A4_ERR_TIMEOUT into the device status word *status (when given),
@@ -183,16 +196,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 // only.  Where a warp's next instructions use the whole warp and the wait is
 // on the critical path it beats lane 0 polling for the others (attention over
 // packed prompts: 375 against 503 us) and each lane polling by itself (408).
+// A try suspends the warp for longer than most waits last, so that a limit
+// of nanoseconds (w4a4_debug_set_wait_limit) may never expire: with HOOK, for
+// waits off the critical path, limits below a microsecond poll instead.
+template <bool HOOK = false>
 __device__ __forceinline__ bool warp_wait_converged(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                     unsigned int* status,
                                                     unsigned long long limit_ns = kWaitLimitNs) {
   const uint32_t at = smem_u32(bar);
-  if (__all_sync(0xFFFFFFFFu, mbar_test(at, parity))) return true;
+  const bool poll = HOOK && limit_ns < 1000ull;
+  if (__all_sync(0xFFFFFFFFu, poll ? mbar_poll(at, parity) : mbar_test(at, parity))) return true;
   const unsigned long long t0 = global_ns();
   while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (__all_sync(0xFFFFFFFFu, mbar_test(at, parity))) return true;
+    for (int i = 0; i < (poll ? 1 : 32); ++i)
+      if (__all_sync(0xFFFFFFFFu, poll ? mbar_poll(at, parity) : mbar_test(at, parity))) return true;
     const bool late = global_ns() - t0 > limit_ns;
     if (late) {
       if (status != nullptr) atomicOr(status, 8u /* W4A4_ERR_TIMEOUT */);

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(WARPS * 32, W16Shape<RT, NT, FEW, WARPS, OFFSE
         sb ^= 1;
         fetch();
       }
-      ok = warp_wait_converged(&full[warp][s], phase, nullptr, a.status, a.wait_ns);
+      ok = warp_wait_converged<true>(&full[warp][s], phase, nullptr, a.status, a.wait_ns);
       if (!ok) break;
       const uint32_t wbase = smem_u32(ring + s * Shape::kStage), xbase = wbase + Shape::kW;
       float sum[RT][NT][4], xs[NT][4];
@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(WARPS * 32, W16Shape<RT, NT, FEW, WARPS, OFFSE
       }
     }
   }
+  cp_async_wait();
   if (!ok && lane == 0)                                // an expired wait: what is in flight lands before the CTA ends
     for (int i = 0; i < kStages; ++i) {
       (void)mbar_wait(&full[warp][i], 0, nullptr, nullptr, 100000000ull);
