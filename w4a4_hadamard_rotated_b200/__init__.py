@@ -3,8 +3,9 @@
 A thin Python binding over the C ABI in ``include/w4a4.h`` (``libw4a4.so``
 next to this file).  The binding only marshals arguments: it checks tensor
 dtypes, devices and layouts, allocates outputs with PyTorch, and passes raw
-device pointers plus the current CUDA stream to the library.  Every step of
-the layer runs in the library's CUDA kernels; there is no CPU or PyTorch
+device pointers plus the current CUDA stream to the library (ctypes here; for
+the entries that run between a block's linears, whose calls are short and
+have many arguments, in the extension _binding.so).  Every step of the layer runs in the library's CUDA kernels; there is no CPU or PyTorch
 fallback, and every call raises if the library is missing or not built.
 
 Functions keep the C names without the ``w4a4_`` prefix:
@@ -75,6 +76,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_native = None          # _binding.so with the library's entry points bound
 
 
 class W4A4Error(RuntimeError):
@@ -85,19 +87,24 @@ class W4A4Error(RuntimeError):
 
 
 def load_library(path=LIB_PATH):
-    """Load libw4a4.so (once) and declare its C signatures."""
-    global _lib
+    """Load libw4a4.so (once), declare its C signatures and hand the block
+    entries' addresses to _binding.so."""
+    global _lib, _native
     if _lib is not None:
         return _lib
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build() "
-                           "(or python w4a4_hadamard_rotated_b200/build.py)")
+    for needed in (path, os.path.join(_HERE, "_binding.so")):
+        if not os.path.exists(needed):
+            raise RuntimeError(f"{needed} is missing: build it with __graft_entry__.build() "
+                               "(or python w4a4_hadamard_rotated_b200/build.py)")
     lib = ctypes.CDLL(path)
     for name, (res, args) in SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    _lib = lib
+    from . import _binding
+    _binding.bind(W4A4Error, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "w4a4_linear_w4a16", "w4a4_qk_norm_rope", "w4a4_attention", "w4a4_attention_workspace_bytes")))
+    _lib, _native = lib, _binding
     return lib
 
 
@@ -373,40 +380,15 @@ def linear_fused_lora(x, Wq, sw, bias, A, B, scale, g=128, out=None):
 # ---- what a transformer block runs between its linears
 #
 # These entries launch on the current stream of the tensors' own device, also
-# when another device is current.
+# when another device is current.  Their arguments are checked and marshalled by
+# _binding.so (csrc/binding.cpp).
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}      # W4A4_BF16, W4A4_FP16
 
 
-def _need_16bit(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
-    return code
-
-
-def _same(t, dtype, shape, name, index):
-    """A contiguous operand of the given type and shape on CUDA device `index`."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
-        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _call(fn, index, args, what):
-    """fn(*args, current stream of CUDA device `index`) with that device current."""
-    if index == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status != OK:
-        raise W4A4Error(status, what)
+def _bound():
+    load_library()
+    return _native
 
 
 def quantize_weight_w4a16(W, group=128, dtype=torch.bfloat16, asymmetric=False):
@@ -425,9 +407,9 @@ def quantize_weight_w4a16(W, group=128, dtype=torch.bfloat16, asymmetric=False):
     Wq = torch.empty(N, K // 2, dtype=torch.int8, device=W.device)
     scale = torch.empty(N, K // group, dtype=dtype, device=W.device)
     offset = torch.empty_like(scale) if asymmetric else None
-    _call(lib.w4a4_quantize_weight_w4a16, W.get_device(),
-          (W.data_ptr(), N, K, W.stride(0), group, _DTYPES[dtype], Wq.data_ptr(), scale.data_ptr(),
-           offset.data_ptr() if asymmetric else None), "w4a4_quantize_weight_w4a16")
+    with torch.cuda.device(W.device):
+        _check(lib.w4a4_quantize_weight_w4a16(_ptr(W), N, K, W.stride(0), group, _DTYPES[dtype], _ptr(Wq), _ptr(scale),
+                                              _ptr(offset), _stream(W)), "w4a4_quantize_weight_w4a16")
     return Wq, scale, offset
 
 
@@ -435,30 +417,7 @@ def linear_w4a16(x, Wq, scale, offset=None, bias=None, out=None):
     """y [M, N] = x W^T (+ bias) for M <= 64 rows of bf16 or fp16 x [M, K] and
     4-bit weights W[n, k] = scale[n, k/group] Wq[n, k] (+ offset[n, k/group]);
     the group is K / scale.shape[1].  scale, offset, bias and y have x's type."""
-    lib = _lib or load_library()
-    code = _need_16bit(x, "x")
-    if x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError("x must be a 2-D tensor with a contiguous inner dimension")
-    M, K = x.shape
-    index, dtype = x.get_device(), x.dtype
-    if not isinstance(Wq, torch.Tensor) or Wq.dim() != 2:
-        raise ValueError("Wq must be a contiguous [N, K/2] int8 tensor on x's device")
-    N = Wq.shape[0]
-    wp = _same(Wq, torch.int8, (N, K // 2), "Wq", index)
-    if not isinstance(scale, torch.Tensor) or scale.dim() != 2 or scale.shape[1] < 1 or K % scale.shape[1] != 0:
-        raise ValueError("scale must be a [N, K/group] tensor")
-    groups = scale.shape[1]
-    sp = _same(scale, dtype, (N, groups), "scale", index)
-    op = None if offset is None else _same(offset, dtype, (N, groups), "offset", index)
-    bp = None if bias is None else _same(bias, dtype, (N,), "bias", index)
-    if out is None:
-        out = x.new_empty((M, N))
-    else:
-        _need_rows(out, dtype, M, N, "out", x.device)
-    _call(lib.w4a4_linear_w4a16, index,
-          (x.data_ptr(), x.stride(0) if M > 1 else K, wp, sp, op, K // groups, bp, out.data_ptr(),
-           out.stride(0) if M > 1 else N, M, N, K, code), "w4a4_linear_w4a16")
-    return out
+    return (_native or _bound()).linear_w4a16(x, Wq, scale, offset, bias, out)
 
 
 def rotary_frequencies(axis_dims, theta=10000.0, device="cuda"):
@@ -476,53 +435,6 @@ def rotary_frequencies(axis_dims, theta=10000.0, device="cuda"):
             torch.tensor(axis, dtype=torch.int32, device=device))
 
 
-def _heads(t, name, shape, dtype, index):
-    """(address, token stride, head stride) of a [T, H, D] tensor with
-    contiguous D; a dimension of one or no element has no stride of its own."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
-        raise TypeError(f"{name} must be a CUDA tensor of {dtype} on cuda:{index}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    T, H, D = shape
-    if t.is_contiguous():
-        return t.data_ptr(), H * D, D
-    st, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    return t.data_ptr(), st if T > 1 else H * D, sh if H > 1 else D
-
-
-def _new_like(t):
-    """A contiguous tensor of t's shape, type and device."""
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
-
-
-def _positions(positions, freq, axis, T, index):
-    """(positions, bits, row stride, axes, freq, axis, R) for the library."""
-    if not isinstance(positions, torch.Tensor) or positions.get_device() != index:
-        raise TypeError("positions must be a CUDA tensor on q's device")
-    if positions.dtype is torch.int32:
-        bits = 32
-    elif positions.dtype is torch.int64:
-        bits = 64
-    else:
-        raise TypeError(f"positions must be torch.int32 or torch.int64, got {positions.dtype}")
-    if positions.dim() not in (1, 2) or positions.shape[0] != T:
-        raise ValueError(f"positions must be [{T}, axes] or [{T}], got {tuple(positions.shape)}")
-    axes = positions.shape[1] if positions.dim() == 2 else 1
-    if axes > 1 and positions.stride(1) != 1:
-        raise ValueError("positions must have a contiguous inner dimension")
-    if freq is None or axis is None:
-        raise ValueError("positions need freq and axis (rotary_frequencies)")
-    half = freq.numel()
-    return (positions.data_ptr(), bits, positions.stride(0) if T > 1 else axes, axes,
-            _same(freq, torch.float64, (half,), "freq", index), _same(axis, torch.int32, (half,), "axis", index),
-            2 * half)
-
-
-_NO_POSITIONS = (None, 0, 0, 0, None, None, 0)
-
-
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, freq=None, axis=None, interleaved=True,
                  eps=1e-6, q_out=None, k_out=None):
     """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (bf16 or fp16)
@@ -532,43 +444,8 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, positions=None, freq=N
       freq [R/2] fp64, axis [R/2] int32: of rotary_frequencies
       interleaved: pairs (2i, 2i + 1), else (i, i + R/2)
       k None: queries only; q_out / k_out may be q / k themselves."""
-    lib = _lib or load_library()
-    code = _need_16bit(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [T, Hq, D]")
-    shape = q.shape
-    T, Hq, D = shape
-    index, dtype = q.get_device(), q.dtype
-    qp, qt, qh = _heads(q, "q", shape, dtype, index)
-    if q_out is None:
-        q_out = _new_like(q)
-        qo = (q_out.data_ptr(), Hq * D, D)
-    else:
-        qo = _heads(q_out, "q_out", shape, dtype, index)
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 3:
-            raise ValueError("k must be [T, Hk, D]")
-        shape = k.shape
-        Hk = shape[1]
-        if shape[0] != T or shape[2] != D:
-            raise ValueError(f"k must be [{T}, Hk, {D}], got {list(shape)}")
-        kp, kt, kh = _heads(k, "k", shape, dtype, index)
-        if k_out is None:
-            k_out = _new_like(k)
-            ko = (k_out.data_ptr(), Hk * D, D)
-        else:
-            ko = _heads(k_out, "k_out", shape, dtype, index)
-    elif k_weight is not None or k_out is not None:
-        raise ValueError("k_weight and k_out need k")
-    else:
-        Hk, kp, kt, kh, ko = 0, None, 0, 0, (None, 0, 0)
-    _call(lib.w4a4_qk_norm_rope, index,
-          (qp, qt, qh, Hq, kp, kt, kh, Hk,
-           None if q_weight is None else _same(q_weight, dtype, (D,), "q_weight", index),
-           None if k_weight is None else _same(k_weight, dtype, (D,), "k_weight", index), eps,
-           *(_NO_POSITIONS if positions is None else _positions(positions, freq, axis, T, index)),
-           1 if interleaved else 0, *qo, *ko, T, D, code), "w4a4_qk_norm_rope")
-    return q_out, k_out
+    return (_native or _bound()).qk_norm_rope(q, k, q_weight, k_weight, positions, freq, axis, interleaved, eps, q_out,
+                                              k_out)
 
 
 def attention(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, causal=False, scale=None, out=None, return_lse=False):
@@ -582,44 +459,7 @@ def attention(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, causal=False, scale
       scale: 1/sqrt(D) unless given
     Rows behind the last sequence keep what `out` held (a new `out` holds
     nothing defined there); queries that see no key get 0 and lse -inf."""
-    lib = _lib or load_library()
-    code = _need_16bit(q, "q")
-    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("q must be [Tq, Hq, D] and k, v [Tk, Hk, D]")
-    qshape, kshape = q.shape, k.shape
-    Tq, Hq, D = qshape
-    Tk, Hk, Dk = kshape
-    if Dk != D:
-        raise ValueError(f"q and k must have the same last dimension, got {D} and {Dk}")
-    index, dtype = q.get_device(), q.dtype
-    qs = _heads(q, "q", qshape, dtype, index)
-    ks = _heads(k, "k", kshape, dtype, index)
-    vs = _heads(v, "v", kshape, dtype, index)
-    if out is None:
-        out = _new_like(q)
-        os_ = (out.data_ptr(), Hq * D, D)
-    else:
-        os_ = _heads(out, "out", qshape, dtype, index)
-    B, cq, ck = 1, None, None
-    if cu_seqlens_q is not None or cu_seqlens_k is not None:
-        if cu_seqlens_q is None or cu_seqlens_k is None:
-            raise ValueError("cu_seqlens_q and cu_seqlens_k go together")
-        B = cu_seqlens_q.numel() - 1
-        if B < 1:
-            raise ValueError("cu_seqlens_q must hold at least two numbers")
-        cq = _same(cu_seqlens_q, torch.int32, (B + 1,), "cu_seqlens_q", index)
-        ck = _same(cu_seqlens_k, torch.int32, (B + 1,), "cu_seqlens_k", index)
-    lse = q.new_empty((Tq, Hq), dtype=torch.float32) if return_lse else None
-    # the workspace is this call's own and lives in PyTorch's allocator (or a
-    # graph's pool) until the stream is past it, so overlapping calls and
-    # captured graphs never share one
-    nbytes = lib.w4a4_attention_workspace_bytes(Tq, Tk, B, Hq, Hk, D)
-    ws = q.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
-    _call(lib.w4a4_attention, index,
-          (*qs, *ks, *vs, *os_, None if lse is None else lse.data_ptr(), cq, ck, B, Tq, Tk, Hq, Hk, D,
-           1 if causal else 0, D ** -0.5 if scale is None else float(scale), code,
-           None if ws is None else ws.data_ptr(), nbytes), "w4a4_attention")
-    return (out, lse) if return_lse else out
+    return (_native or _bound()).attention(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out, return_lse)
 
 
 def debug_set_wait_limit(limit_ns):

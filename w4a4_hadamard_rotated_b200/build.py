@@ -3,7 +3,9 @@
 Each CUDA source compiles to an object in parallel; the objects link into one
 shared library next to this file.  The CUDA runtime is linked statically, and
 the driver's tensor-map encoder is resolved at run time, so the library
-needs no libcuda at link time and builds on a machine without a GPU.
+needs no libcuda at link time and builds on a machine without a GPU.  The
+CPython extension _binding.so (csrc/binding.cpp, plain C++ over PyTorch's
+headers) is built beside it with g++.
 """
 
 import os
@@ -18,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libw4a4.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "quant.cu", "quant_tc.cu", "gemm.cu", "gemm_legacy.cu", "smallm.cu", "gemv.cu", "noalloc.cu", "lora.cu",
            "w4a16.cu", "qk_rope.cu", "attention.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -42,6 +45,29 @@ def _up_to_date(obj, deps):
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def build_binding(force=False):
+    """_binding.so: the marshalling of the block entries."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and _up_to_date(BINDING, [src, os.path.join(INCLUDE, "w4a4.h")]):
+        return BINDING
+    root = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), src, "-o", BINDING,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return BINDING
+
+
 def build(verbose=False, force=False, ptxas_verbose=False):
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -60,8 +86,10 @@ def build(verbose=False, force=False, ptxas_verbose=False):
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_verbose:
         for _, log in results:
