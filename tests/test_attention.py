@@ -131,6 +131,23 @@ def test_many_short_sequences(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B", [127, 128, 129, 1000])
+def test_many_decoded_sequences(cuda_lib, B):
+    """More sequences than a warp walks at a time, some without queries or keys."""
+    gen = torch.Generator().manual_seed(B)
+    qs = torch.randint(0, 3, (B,), generator=gen).tolist()
+    ks = torch.randint(0, 200, (B,), generator=gen).tolist()
+    q, k, v = make(sum(qs), sum(ks), 4, 2, 64, torch.bfloat16)
+    out, lse = w4.attention(q, k, v, cu(qs), cu(ks), causal=True, return_lse=True)
+    pick = [i for i in range(B) if i % 37 in (0, 5, 36) or i > B - 4]
+    at_q, at_k = [0] + torch.tensor(qs).cumsum(0).tolist(), [0] + torch.tensor(ks).cumsum(0).tolist()
+    rows = torch.cat([torch.arange(at_q[i], at_q[i + 1]) for i in pick]).cuda()
+    keys = torch.cat([torch.arange(at_k[i], at_k[i + 1]) for i in pick]).cuda()
+    check(out[rows], lse[rows], q[rows], k[keys], v[keys], [qs[i] for i in pick], [ks[i] for i in pick], True)
+    assert torch.isfinite(out).all() and w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
 def test_long_prompt(cuda_lib, causal):
     go([4500], [4500], 2, 2, 128, torch.bfloat16, causal)

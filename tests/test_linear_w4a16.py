@@ -238,3 +238,16 @@ def test_expired_waits_end_the_call(cuda_lib):
     for (x, c, s, o, _), g in zip(cases, good):
         assert torch.equal(w4.linear_w4a16(x, c, s, offset=o), g)
     assert w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 2, 3, 8])
+@pytest.mark.parametrize("K,N", [(4096, 1000), (4096, 4090), (5120, 5000), (640, 9000), (1536, 2300), (9600, 33)])
+@pytest.mark.parametrize("group,offset", [(32, True), (64, False), (128, True)])
+def test_every_split_of_rows_and_warps(cuda_lib, M, K, N, group, offset):
+    """Shapes that take 16 or 32 rows and 8 or 16 warps a CTA, several tiles and ragged ones."""
+    args = make(M, K, N, group, torch.bfloat16, offset, True, seed=N)
+    x, codes, scale, off, b = on_gpu(*args)
+    y = w4.linear_w4a16(x, codes, scale, offset=off, bias=b)
+    # the reference on the GPU, in float64
+    check(y, *[t.cpu() for t in reference(x, codes, scale, off, b)], K)

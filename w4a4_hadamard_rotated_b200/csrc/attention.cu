@@ -90,22 +90,29 @@ struct Place {
 };
 
 // The place of block `index`: sequences in order, each with its query tiles
-// times its key chunks.  A warp walks the sequences 32 at a time.
+// times its key chunks.  A warp walks the sequences 32 kEach at a time.
+template <int kEach>
 __device__ __forceinline__ bool find_place(const AttnArgs& a, int index, int tokens, int chunk_tiles, Place& p) {
   const int lane = threadIdx.x & 31;
   int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    int q0 = 0, nq = 0, k0 = 0, nk = 0, n = 0, chunks = 1;
-    if (b < a.B) {
-      q0 = cu_at(a.cu_q, b, a.Tq);
-      nq = max(cu_at(a.cu_q, b + 1, a.Tq) - q0, 0);
-      k0 = cu_at(a.cu_k, b, a.Tk);
-      nk = max(cu_at(a.cu_k, b + 1, a.Tk) - k0, 0);
-      if (chunk_tiles != 0) chunks = max(1, ((nk + kTile - 1) / kTile + chunk_tiles - 1) / chunk_tiles);
-      n = (nq + tokens - 1) / tokens * chunks;
+  for (int b0 = 0; b0 < a.B; b0 += 32 * kEach) {
+    const int b = b0 + lane * kEach;
+    int cq[kEach + 1], ck[kEach + 1];
+#pragma unroll
+    for (int i = 0; i <= kEach; ++i) {
+      cq[i] = b + i <= a.B ? cu_at(a.cu_q, b + i, a.Tq) : 0;
+      ck[i] = b + i <= a.B ? cu_at(a.cu_k, b + i, a.Tk) : 0;
     }
-    int incl = n;
+    int n[kEach], chunks[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int nq = max(cq[i + 1] - cq[i], 0), nk = max(ck[i + 1] - ck[i], 0);
+      chunks[i] = 1;
+      if (chunk_tiles != 0) chunks[i] = max(1, ((nk + kTile - 1) / kTile + chunk_tiles - 1) / chunk_tiles);
+      n[i] = b + i < a.B ? (nq + tokens - 1) / tokens * chunks[i] : 0;
+      sum += n[i];
+    }
+    int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -113,13 +120,22 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int index, int tok
     }
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > index);
     if (hit != 0) {
+      // the block's sequence among the four of this lane, if it is this lane
+      int at = index - (before + incl - sum), i = 0;
+      for (; i < kEach - 1 && at >= n[i]; ++i) at -= n[i];
+      int q0 = cq[0], q1 = cq[1], k0 = ck[0], k1 = ck[1], ch = chunks[0], most = n[0];
+#pragma unroll
+      for (int j = 1; j < kEach; ++j)
+        if (i == j) q0 = cq[j], q1 = cq[j + 1], k0 = ck[j], k1 = ck[j + 1], ch = chunks[j], most = n[j];
       const int src = __ffs(hit) - 1;
-      const int at = index - (before + __shfl_sync(0xFFFFFFFFu, incl - n, src));
-      const int ch = __shfl_sync(0xFFFFFFFFu, chunks, src);
+      at = __shfl_sync(0xFFFFFFFFu, at, src);
+      most = __shfl_sync(0xFFFFFFFFu, most, src);
+      ch = __shfl_sync(0xFFFFFFFFu, ch, src);
       p.q0 = __shfl_sync(0xFFFFFFFFu, q0, src);
-      p.nq = __shfl_sync(0xFFFFFFFFu, nq, src);
+      p.nq = max(__shfl_sync(0xFFFFFFFFu, q1, src) - p.q0, 0);
       p.k0 = __shfl_sync(0xFFFFFFFFu, k0, src);
-      p.nk = __shfl_sync(0xFFFFFFFFu, nk, src);
+      p.nk = max(__shfl_sync(0xFFFFFFFFu, k1, src) - p.k0, 0);
+      if (at < 0 || at >= most) return false;        // lengths whose sums do not fit an int
       p.tile = at / ch;
       p.chunk = at - p.tile * ch;
       return true;
@@ -313,7 +329,8 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
     // long causal tiles first: the block order runs backwards
     const int index = a.causal ? static_cast<int>(gridDim.x - 1 - blockIdx.x) : static_cast<int>(blockIdx.x);
     Place p{};
-    const bool found = find_place(a, index, NQ * a.tokens, SPLIT ? a.chunk : 0, p);
+    const bool found = a.B <= 32 ? find_place<1>(a, index, NQ * a.tokens, SPLIT ? a.chunk : 0, p)
+                                 : find_place<4>(a, index, NQ * a.tokens, SPLIT ? a.chunk : 0, p);
     if (lane == 0) {
       bars.place = p;
       bars.found = found;

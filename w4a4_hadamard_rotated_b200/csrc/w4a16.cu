@@ -267,6 +267,11 @@ __global__ void __launch_bounds__(WARPS * 32, W16Shape<RT, NT, FEW, WARPS, OFFSE
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
   }
+  // the first stages' codes on their way into L2 while the previous kernel of the
+  // stream ends (a prefetch reads nothing into this kernel)
+  if (lane < kStages && lane < n)
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&tmW)),
+                 "r"((u0 + lane) * (kW16Cols / 2)), "r"(static_cast<int>(blockIdx.x) * kRows) : "memory");
   __syncwarp();
   griddep_wait();
   griddep_launch_dependents();
@@ -487,16 +492,37 @@ cudaError_t launch_w16(const W16Call& c, W16Args a) {
   return cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, a);
 }
 
+// Rows and warps of a CTA.  16 warps share an SM either way: two CTAs of 8, or
+// one of 16, which halves the slices of k.  A warp's stage of 32 rows takes 1.6
+// times as long as one of 16, a tile about 1.5 of the former besides its
+// stages, and the tiles run in rounds of what the GPU holds: take the least.
+// Measured against one another: 1x4096->4096 32 rows x 16 warps 4.3, 16 x 8 5.0 us;
+// 1x4096->1024 16 x 16 3.6, 16 x 8 4.1; 8x12288->3072 32 x 16 11.2, 16 x 8 12.8, 32 x 8 12.9;
+// 4x5120->5120 32 x 8 9.2, 32 x 16 10.7; 1x5120->30720 32 x 8 27, 16 x 8 32, 32 x 16 31.
+template <class T, int NT, bool FEW, int GROUP, bool OFFSET>
+cudaError_t launch_w16_tiles(const W16Call& c, const W16Args& a) {
+  const int units = (a.K + kW16Cols - 1) / kW16Cols;
+  int best = 0;
+  float least = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    const int rows = i & 1 ? 32 : 16, warps = i & 2 ? 16 : 8, at_once = c.num_sms * 16 / warps;
+    const int rounds = ((a.N + rows - 1) / rows + at_once - 1) / at_once;
+    const float cost = rounds * ((units + warps - 1) / warps * (i & 1 ? 1.f : 0.62f) + 1.5f);
+    if (i == 0 || cost < least) least = cost, best = i;
+  }
+  switch (best) {
+    case 0: return launch_w16<T, 1, NT, FEW, 8, GROUP, OFFSET>(c, a);
+    case 1: return launch_w16<T, 2, NT, FEW, 8, GROUP, OFFSET>(c, a);
+    case 2: return launch_w16<T, 1, NT, FEW, 16, GROUP, OFFSET>(c, a);
+    default: return launch_w16<T, 2, NT, FEW, 16, GROUP, OFFSET>(c, a);
+  }
+}
+
 template <class T, int GROUP, bool OFFSET>
 cudaError_t launch_w16_rows(const W16Call& c, const W16Args& a) {
-  if (a.M <= 2) {
-    if (a.N < 64 * c.num_sms) return launch_w16<T, 1, 1, true, 8, GROUP, OFFSET>(c, a);
-    return launch_w16<T, 2, 1, true, 8, GROUP, OFFSET>(c, a);
-  }
-  if (a.M <= 8) {
-    if (a.N < 64 * c.num_sms) return launch_w16<T, 2, 1, false, 16, GROUP, OFFSET>(c, a);
-    return launch_w16<T, 2, 1, false, 8, GROUP, OFFSET>(c, a);
-  }
+  if (a.M <= 2) return launch_w16_tiles<T, 1, true, GROUP, OFFSET>(c, a);
+  if (a.M <= 8) return launch_w16_tiles<T, 1, false, GROUP, OFFSET>(c, a);
+  // more rows of x than weights per stage: two CTAs do not fit an SM
   return launch_w16<T, 2, 2, false, 12, GROUP, OFFSET>(c, a);
 }
 
