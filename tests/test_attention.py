@@ -124,6 +124,19 @@ def test_single_tokens_over_long_caches(cuda_lib, Hq, Hk, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 128), (torch.float16, 64)], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("qs,ks,Hq,Hk", [
+    ([300], [6000], 1, 1),                             # several query tiles and many chunks
+    ([700, 1, 260], [3000, 900, 2100], 6, 2),
+    ([130, 0, 5], [40, 3000, 7000], 5, 1),             # rows that see nothing, a sequence without queries
+    ([2500], [2500], 1, 1),
+])
+def test_few_tiles_over_many_keys(cuda_lib, dtype, D, causal, qs, ks, Hq, Hk):
+    go(qs, ks, Hq, Hk, D, dtype, causal, seed=sum(ks))
+
+
+@pytest.mark.gpu
 def test_many_short_sequences(cuda_lib):
     gen = torch.Generator().manual_seed(1)
     n = torch.randint(0, 40, (300,), generator=gen).tolist()

@@ -37,6 +37,10 @@
 //   * Few rows (SPLIT): the keys of a sequence are cut into chunks, one CTA
 //     each (NQ = 1, two CTAs per SM); they write O and lse in fp32 to the
 //     workspace and attention_join_kernel weighs them by e^(lse_c - lse).
+// Measured (bf16, D 128, graph replays): 4608 x 24 heads 220 us, 1.18 PF/s;
+// 32760 x 10 heads 4.63 ms, 1.16 PF/s (the board's power limit holds the clock
+// at 1.75 GHz); eight causal prompts, 11168 tokens x 40/8 heads, fp16 381 us,
+// 0.9 PF/s; 8 tokens x 32/8 heads over 66796 keys 58 us, 4.7 TB/s.
 //   Every wait is bounded; an expired wait records W4A4_ERR_TIMEOUT, every
 //   role stops, copies and MMAs drain and tensor memory is freed.
 #include <cuda.h>
@@ -656,15 +660,17 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
 }
 
 // out = sum_c e^(lse_c - lse) O_c over the chunks of a row's keys, lse = log
-// sum_c e^(lse_c); one warp per (token, head), chunks in order.
-template <class T, int D>
+// sum_c e^(lse_c).  WARPS (1 or 4) warps share a (token, head) row, every
+// WARPS-th chunk each, and meet in shared memory in order.
+template <class T, int D, int WARPS>
 __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
   constexpr int E = D / 32;
+  __shared__ float met[4][D + 1];
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * (4 / WARPS) + warp / WARPS;
   const int64_t rows = static_cast<int64_t>(a.Tq) * a.Hq;
-  if (w >= rows) return;
+  if (w >= rows) return;                             // WARPS == 4: the whole block
   const int tok = static_cast<int>(w / a.Hq);
   const int head = static_cast<int>(w - static_cast<int64_t>(tok) * a.Hq);
   Place p{};
@@ -678,7 +684,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
   const float base = top == -INFINITY ? 0.f : top;
   float sum = 0.f, acc[E] = {};
 #pragma unroll 4
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = warp % WARPS; c < chunks; c += WARPS) {
     const float z = a.part_lse[c * rows + w];
     if (z == -INFINITY) continue;                    // a chunk of which nothing is seen
     const float f = ex2(z - base);
@@ -686,6 +692,19 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
     const float* o = a.part_o + (c * rows + w) * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(f, o[e], acc[e]);
+  }
+  if (WARPS > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) met[warp][lane * E + e] = acc[e];
+    if (lane == 0) met[warp][D] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int v = 1; v < WARPS; ++v) {
+      sum += met[v][D];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += met[v][lane * E + e];
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t* out = reinterpret_cast<uint32_t*>(a.out + tok * a.o_t + head * a.o_h + lane * E);
@@ -720,11 +739,30 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
   p.blocks = p.nq == 1 ? Tq / p.tokens + B : Tq / (2 * p.tokens) + B;
   p.chunks = 1;
   if (p.nq == 1 && one < 296) {
-    // about two rounds of two blocks per SM, chunks of four key tiles at least
-    const int64_t tiles = (Tk + kTile - 1) / kTile;
-    int64_t chunk = (tiles * one + B * 592 - 1) / (B * 592);
-    if (chunk < 4) chunk = 4;
-    if (chunk * B < tiles) {
+    const int64_t tiles = (Tk + kTile - 1) / kTile, each = (tiles + B - 1) / B;
+    int64_t chunk = 0;
+    if (Tq <= B * p.tokens) {
+      // One query tile a sequence: the keys' bytes are the work.  About two
+      // rounds of two blocks per SM (8 tokens over 66796 keys: 58 us; one
+      // round 66, three 60, four 63), chunks of two tiles at least (1 token
+      // over 32768 keys: 14.4 us; of one 20.5, of four 15.2)
+      chunk = (tiles * one + B * 592 - 1) / (B * 592);
+      if (chunk < 2) chunk = 2;
+    } else {
+      // More than one: the keys are shared through L2.  Microseconds: 1.6 a
+      // tile while each block has an SM, else 2.2, 5 to begin and end a block;
+      // 4 for the join and the partial outputs twice through HBM.  In one
+      // piece and in two: 16384 queries x 1 head 210 us and 139, 2048 x 8
+      // heads 31 and 44 (chunks of four tiles)
+      float least = 0.f;
+      for (int64_t n = 1; n <= 16; ++n) {
+        const int64_t c = (each + n - 1) / n, blocks = one * n;
+        const float cost = ((blocks + 295) / 296) * (c * (blocks <= 148 ? 1.6f : 2.2f) + 5.f) +
+                           (n > 1 ? 4.f + n * Tq * Hq * 1.6e-4f : 0.f);
+        if (n == 1 || cost < least) least = cost, chunk = n == 1 ? 0 : c;
+      }
+    }
+    if (chunk != 0 && chunk * B < tiles) {
       p.chunk = static_cast<int>(chunk);
       const int64_t most = (Tq + p.tokens - 1) / p.tokens;      // query tiles of one sequence
       const int64_t x = most * (tiles / chunk + B), y = (Tq / p.tokens + B) * (tiles / chunk + 1);
@@ -756,7 +794,7 @@ int heads_map(CUtensorMap* map, const void* base, bool bf16, int64_t T, int64_t 
 
 template <class T, int D, int NQ, bool SPLIT>
 cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnArgs& a,
-                      int64_t blocks, int64_t sets, cudaStream_t stream) {
+                      int64_t blocks, int64_t sets, int64_t chunks, cudaStream_t stream) {
   using Shape = AttnShape<D, NQ>;
   auto kernel = attention_tc_kernel<T, D, NQ, SPLIT>;
   static bool attr_set[64] = {};
@@ -784,19 +822,25 @@ cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUte
   e = cudaLaunchKernelEx(&cfg, kernel, tmQ, tmK, tmV, a);
   if (e != cudaSuccess || !SPLIT) return e;
   const int64_t rows = static_cast<int64_t>(a.Tq) * a.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4), 1, 1);
   cfg.blockDim = dim3(128, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D>, a);
+  // chunks of one sequence at most.  A warp and four a row: 128 chunks of one
+  // token 34.5 us and 14.4 with the attention, two of 16384 139 us and 155
+  if (chunks > 8) {
+    cfg.gridDim = dim3(static_cast<unsigned>(rows), 1, 1);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D, 4>, a);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4), 1, 1);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D, 1>, a);
 }
 
 template <class T, int D>
 cudaError_t launch_plan(const Plan& p, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                         const AttnArgs& a, cudaStream_t stream) {
   const int64_t sets = a.Hq / p.G;
-  if (p.chunk != 0) return launch_tc<T, D, 1, true>(tmQ, tmK, tmV, a, p.blocks, sets, stream);
-  if (p.nq == 1) return launch_tc<T, D, 1, false>(tmQ, tmK, tmV, a, p.blocks, sets, stream);
-  return launch_tc<T, D, 2, false>(tmQ, tmK, tmV, a, p.blocks, sets, stream);
+  if (p.chunk != 0) return launch_tc<T, D, 1, true>(tmQ, tmK, tmV, a, p.blocks, sets, p.chunks, stream);
+  if (p.nq == 1) return launch_tc<T, D, 1, false>(tmQ, tmK, tmV, a, p.blocks, sets, p.chunks, stream);
+  return launch_tc<T, D, 2, false>(tmQ, tmK, tmV, a, p.blocks, sets, p.chunks, stream);
 }
 
 }  // namespace

@@ -5,7 +5,7 @@
 // Every weight is used once per row of x: N K / 2 bytes of codes and 2 N K / group
 // of scales against 2 M N K flops, bound by the weight stream up to the largest M.
 //
-// Design (linear_w4a16_kernel<T, RT, NT, GROUP, OFFSET>)
+// Design (linear_w4a16_kernel<T, RT, NT, FEW, WARPS, GROUP, OFFSET>)
 //   * Warp-level mma.m16n8k16 with fp32 sums: the weights are the 16-row A
 //     operand, x the 8-column B operand.  One instruction per 256 weights
 //     leaves the issue slots to the widening, the dearest part (11 per 8 codes);
@@ -22,15 +22,17 @@
 //     0, 1 and 2, 3 swap a word, so that an instruction stays inside a group.
 //   * Sums of x per group (offsets) come from one more product per step with
 //     an A operand of ones, shared by the RT row tiles.
-//   * A warp takes RT tiles of 16 weight rows and a slice of k; the 8 warps
-//     of a CTA and the CTAs of a cluster split k, so that a few thousand rows
-//     fill the GPU too, and their partial sums meet in shared memory in a
-//     fixed order (no atomics).  More activation rows want more weight rows
-//     per warp, since x is read once per warp.
+//   * A warp takes RT tiles of 16 weight rows and a slice of k; the 8, 12 or
+//     16 warps of a CTA split k, and their partial sums meet in shared memory
+//     in a fixed order (no atomics).  More activation rows want more weight
+//     rows per warp, since x is read once per warp.
 //   * Each warp feeds itself: a ring of stages of 128 columns that TMA boxes
 //     fill (weights 64 bytes a row, x 64 columns a row, both swizzled so that
 //     the operand reads are free of bank conflicts; what is out of range
 //     arrives as zeros), one lane issuing, no barrier between warps.
+// Measured (graph replays): 1 x 3072 -> 3072 4.4 us, 1 x 5120 -> 30720 26 us
+// (3.2 TB/s, the widening's issue slots), 8 x 12288 -> 3072 with offsets 11.3 us,
+// 16 x 5120 -> 13824 of groups of 32 25.6 us.
 //   Every wait is bounded; an expired one records W4A4_ERR_TIMEOUT, ends the
 //   warp's sums early and lets its copies land.
 #include <cuda.h>
