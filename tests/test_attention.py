@@ -137,6 +137,32 @@ def test_few_tiles_over_many_keys(cuda_lib, dtype, D, causal, qs, ks, Hq, Hk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("qs,ks,Hq,Hk", [
+    ([1] * 40, [20000] + [100 + 7 * i for i in range(39)], 16, 4),   # one cache far longer than the rest
+    ([1] * 64, [2000] * 64, 8, 1),                                   # a block walks over several places
+    ([1, 0, 4, 2, 1] * 40, [300, 70, 1500, 0, 2600] * 40, 8, 1),
+    ([3] * 20, [4100] * 20, 24, 1),                                  # a head set of 24
+])
+def test_decoded_batches(cuda_lib, qs, ks, Hq, Hk):
+    go(qs, ks, Hq, Hk, 64 if Hk == 4 else 128, torch.bfloat16, True, seed=len(qs))
+
+
+@pytest.mark.gpu
+def test_expired_waits_of_a_decoded_batch(cuda_lib):
+    q, k, v = make(64, 64 * 2000, 8, 1, 128, torch.bfloat16)
+    cq, ck = cu([1] * 64), cu([2000] * 64)
+    good = w4.attention(q, k, v, cq, ck, causal=True)
+    w4.debug_set_wait_limit(5)
+    try:
+        w4.attention(q, k, v, cq, ck, causal=True)
+        assert w4.last_device_error() == 8
+    finally:
+        w4.debug_set_wait_limit(0)
+    assert torch.equal(w4.attention(q, k, v, cq, ck, causal=True), good)
+    assert w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_many_short_sequences(cuda_lib):
     gen = torch.Generator().manual_seed(1)
     n = torch.randint(0, 40, (300,), generator=gen).tolist()

@@ -81,6 +81,24 @@ def test_attention_refuses(lib, change, status):
     assert lib.w4a4_attention(*{**ATTN, **change}.values()) == status
 
 
+@pytest.mark.parametrize("Tq,Tk,B,Hq,Hk,D", [
+    (0, 10, 1, 8, 8, 128), (-1, 10, 1, 8, 8, 128), (1, -1, 1, 8, 8, 128), (1, 10, 0, 8, 8, 128), (1, 10, 1, 8, 3, 128),
+    (1, 10, 1, 0, 1, 128), (1, 10, 1, 8, 0, 128), (1, 10, 1, 8, 8, 0), (2 ** 62, 2 ** 62, 1, 8, 8, 128),
+    (1, 2 ** 62, 1, 8, 8, 128), (1, 2 ** 20, 2 ** 60, 8, 8, 128), (1, 2 ** 20, 2 ** 62, 2 ** 62, 1, 128),
+    (1, 2 ** 20, 1, 8, 8, 2 ** 62)])
+def test_attention_workspace_of_sizes_that_are_refused(lib, Tq, Tk, B, Hq, Hk, D):
+    """Sizes past the limits, up to those whose products do not fit 64 bits."""
+    assert lib.w4a4_attention_workspace_bytes(Tq, Tk, B, Hq, Hk, D) == 0
+
+
+@pytest.mark.parametrize("Tq,Tk,B,Hq,Hk,D", [
+    (1, 2 ** 30, 1, 8, 1, 128), (2 ** 24, 2 ** 30, 2 ** 24, 8, 1, 128), (2 ** 30, 2 ** 30, 1, 65535, 1, 64),
+    (200 * 32, 200 * 2 ** 17, 200, 8, 8, 128), (1024, 1024 * 1000, 1024, 32, 8, 128)])
+def test_attention_workspace_stays_small(lib, Tq, Tk, B, Hq, Hk, D):
+    """Beside the keys, for a few queries a sequence: 128 MB and a little."""
+    assert lib.w4a4_attention_workspace_bytes(Tq, Tk, B, Hq, Hk, D) <= 129 * 2 ** 20
+
+
 def test_binding_refuses_host_tensors_and_other_types():
     h = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     calls = [

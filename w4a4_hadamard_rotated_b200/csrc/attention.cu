@@ -8,7 +8,7 @@
 // prompts the tensor cores and the exponentials bound it, over a cache for
 // few queries the bytes of k and v.
 //
-// Design (attention_tc_kernel<T, D, NQ, SPLIT>)
+// Design (attention_tc_kernel<T, D, NQ, SPLIT, FEW>)
 //   * A CTA owns NQ tiles of 128 query rows of one key head and walks 128-key
 //     tiles.  The rows of a tile are (token, head) pairs: G heads that read
 //     the same key head times 128 / G tokens (one 3-D TMA box), so grouped
@@ -34,18 +34,25 @@
 //   * Masks select (-inf) rather than add, on the tiles they cut only.  Value
 //     rows behind a sequence's end inside its last tile are zeroed in
 //     shared memory, so whatever lies there reaches nothing.
-//   * Few rows (SPLIT): the keys of a sequence are cut into chunks, one CTA
+//   * Few tiles (SPLIT): the keys of a sequence are cut into chunks, one CTA
 //     each (NQ = 1, two CTAs per SM); they write O and lse in fp32 to the
-//     workspace and attention_join_kernel weighs them by e^(lse_c - lse).
+//     workspace and attention_join_kernel weighs them by e^(lse_c - lse).  A
+//     sequence of one chunk is written at once.
+//   * Few rows (FEW), a token or some over caches: the tile keeps 32 rows of q
+//     in shared memory and one softmax warp, and the ring holds a third k or v
+//     tile instead of the other 96 rows; the MMAs still run over 128 rows, those
+//     behind the 32 of whatever lies there and read by nobody (8 tokens over 66796
+//     keys: 50 us; with 128 rows, four warps and two tiles 58).
 // Measured (bf16, D 128, graph replays): 4608 x 24 heads 220 us, 1.18 PF/s;
 // 32760 x 10 heads 4.63 ms, 1.16 PF/s (the board's power limit holds the clock
 // at 1.75 GHz); eight causal prompts, 11168 tokens x 40/8 heads, fp16 381 us,
-// 0.9 PF/s; 8 tokens x 32/8 heads over 66796 keys 58 us, 4.7 TB/s.
+// 0.9 PF/s; 8 tokens x 32/8 heads over 66796 keys 51 us, 5.4 TB/s.
 //   Every wait is bounded; an expired wait records W4A4_ERR_TIMEOUT, every
 //   role stops, copies and MMAs drain and tensor memory is freed.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -59,6 +66,7 @@ namespace w4a4 {
 namespace {
 
 constexpr int kTile = 128;             // query rows per MMA tile and keys per key tile
+constexpr int kFewRows = 32;           // query rows of a tile of few
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;        // how far (log2) the maximum in use may fall behind
@@ -75,6 +83,7 @@ struct AttnArgs {
   int causal;
   float scale_log2;                    // scale * log2 e
   int chunk;                           // SPLIT: key tiles per chunk
+  int blocks;                          // SPLIT: upper bound of a head set's places
   float* part_o;                       // SPLIT: [chunks][Tq][Hq][D]
   float* part_lse;                     // SPLIT: [chunks][Tq][Hq], log2 units
   unsigned int* status;
@@ -149,12 +158,17 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int index, int tok
   return false;
 }
 
-// The sequence that holds query row `row`.
+// The sequence that holds query row `row`: the last that begins at or before
+// it, by a warp that looks at 32 at a time.
 __device__ __forceinline__ bool find_token(const AttnArgs& a, int row, Place& p) {
-  int lo = 0, hi = a.B;                // the last sequence that begins at or before the row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (cu_at(a.cu_q, mid, a.Tq) <= row) lo = mid; else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, among = a.B;
+  while (among > 1) {
+    const int step = (among + 31) / 32;
+    const bool in = lane * step < among && cu_at(a.cu_q, lo + lane * step, a.Tq) <= row;
+    const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, in) | 1u);
+    lo += last * step;
+    among = min(step, among - last * step);
   }
   p.q0 = cu_at(a.cu_q, lo, a.Tq);
   p.nq = cu_at(a.cu_q, lo + 1, a.Tq) - p.q0;
@@ -163,16 +177,20 @@ __device__ __forceinline__ bool find_token(const AttnArgs& a, int row, Place& p)
   return row >= p.q0 && row < p.q0 + p.nq;
 }
 
-template <int D, int NQ>
+template <int D, int NQ, bool FEW>
 struct AttnShape {
   static constexpr int kChunks = D / 64;                        // 64-column boxes of a row
   static constexpr uint32_t kBox = kTile * 128;                 // 16 KB: 128 rows of 64 columns
-  static constexpr uint32_t kQBytes = NQ * kChunks * kBox;
+  static constexpr uint32_t kQBox = FEW ? kFewRows * 128 : kBox;
+  static constexpr uint32_t kQBytes = NQ * kChunks * kQBox;
   static constexpr uint32_t kSlot = kChunks * kBox;             // one k or v tile
-  static constexpr int kSlots = NQ == 1 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 8);
+  static constexpr int kSlots = FEW ? (D == 128 ? 3 : 6) : NQ == 1 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 8);
   static constexpr uint32_t kSmem = kQBytes + kSlots * kSlot + 1024;
   static constexpr uint32_t kTmemCols = NQ == 1 ? 256 : 512;
-  static constexpr int kThreads = (NQ * 4 + 2) * 32;
+  static constexpr int kSoftmaxWarps = FEW ? 1 : 4;             // per query tile
+  static constexpr int kThreads = (NQ * kSoftmaxWarps + 2) * 32;
+  // FEW: an MMA reads 128 rows of q all the same, those behind the box out of the ring
+  static_assert((kChunks - 1) * kQBox + kBox <= kQBytes + kSlots * kSlot, "");
   static __device__ constexpr uint32_t s_col(int t) { return t * kTile; }
   static __device__ constexpr uint32_t o_col(int t) { return NQ * kTile + t * D; }
 };
@@ -283,11 +301,11 @@ __device__ __forceinline__ void weigh32(uint32_t (&s)[32], uint64_t cc, uint64_t
   }
 }
 
-template <class T, int D, int NQ, bool SPLIT>
-__global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
+template <class T, int D, int NQ, bool SPLIT, bool FEW>
+__global__ void __launch_bounds__(AttnShape<D, NQ, FEW>::kThreads, NQ == 1 ? 2 : 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
-  using Shape = AttnShape<D, NQ>;
+  using Shape = AttnShape<D, NQ, FEW>;
   constexpr int kSlots = Shape::kSlots;
   constexpr bool kBf16 = std::is_same<T, Bf16>::value;
   extern __shared__ uint8_t smem_dyn[];
@@ -296,8 +314,8 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
   uint8_t* ring = smem + Shape::kQBytes;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  constexpr int kMmaWarp = NQ * 4;
-  constexpr int kLoadWarp = NQ * 4 + 1;
+  constexpr int kMmaWarp = NQ * Shape::kSoftmaxWarps;
+  constexpr int kLoadWarp = kMmaWarp + 1;
 
   // q, k, v and the lengths may be the previous kernel's output (launched
   // with programmatic stream serialization)
@@ -311,8 +329,8 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
       mbar_init(&bars.tail, 1);
       for (int t = 0; t < NQ; ++t) {
         mbar_init(&bars.s_full[t], 1);
-        mbar_init(&bars.p_half[t], 4);
-        mbar_init(&bars.p_full[t], 4);
+        mbar_init(&bars.p_half[t], Shape::kSoftmaxWarps);
+        mbar_init(&bars.p_full[t], Shape::kSoftmaxWarps);
         mbar_init(&bars.o_full[t], 1);
       }
       mbar_init(&bars.drain, 1);
@@ -329,25 +347,35 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
     tmem_relinquish();
   }
   griddep_wait();
-  if (warp == 0) {
-    // long causal tiles first: the block order runs backwards
-    const int index = a.causal ? static_cast<int>(gridDim.x - 1 - blockIdx.x) : static_cast<int>(blockIdx.x);
-    Place p{};
-    const bool found = a.B <= 32 ? find_place<1>(a, index, NQ * a.tokens, SPLIT ? a.chunk : 0, p)
-                                 : find_place<4>(a, index, NQ * a.tokens, SPLIT ? a.chunk : 0, p);
-    if (lane == 0) {
-      bars.place = p;
-      bars.found = found;
+  // Long causal tiles first: the block order runs backwards.  FEW and SPLIT:
+  // the host knows an upper bound of the places only, far above their number
+  // when it is not one sequence that has all queries and keys; so a block walks
+  // over places, the grid's size apart (64 tokens over 64 caches of 2000:
+  // 22 us, a block for each possible place 40).  The barriers go on from place to place.
+  int index = static_cast<int>(blockIdx.x);
+  if (!SPLIT && a.causal) index = static_cast<int>(gridDim.x) - 1 - index;
+  uint32_t tiles_done = 0, places_done = 0;          // key tiles, places with keys
+  uint32_t loads = 0, tails = 0;                     // producer: ring loads, cut tiles
+  int slot = 0;                                      // MMA: of the k tile last used
+  uint32_t phase = 0;
+  while (true) {
+    if (warp == 0) {
+      Place p{};
+      const bool found = a.B <= 32 ? find_place<1>(a, index, NQ * a.tokens, SPLIT ? a.chunk : 0, p)
+                                   : find_place<4>(a, index, NQ * a.tokens, SPLIT ? a.chunk : 0, p);
+      if (lane == 0) {
+        bars.place = p;
+        bars.found = found;
+      }
     }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  griddep_launch_dependents();
-  const uint32_t tmem_base = bars.tmem_base;
-  const Place pl = bars.place;
-  volatile int* abort_flag = &bars.abort_flag;
-  if (bars.found) {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();
+    if (!bars.found) break;
+    const uint32_t tmem_base = bars.tmem_base;
+    const Place pl = bars.place;
+    volatile int* abort_flag = &bars.abort_flag;
     // key head, its first query head, and the tokens of the block
     const int kh = static_cast<int>(blockIdx.y) / a.groups;
     const int h0 = static_cast<int>(blockIdx.y) * a.G;
@@ -379,15 +407,14 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
           for (int t = 0; t < NQ; ++t) {
             if (n[t] == 0) continue;
             for (int c = 0; c < Shape::kChunks; ++c)
-              tma_load_3d(smem + (t * Shape::kChunks + c) * Shape::kBox, &tmQ, &bars.q_full, 64 * c, h0,
+              tma_load_3d(smem + (t * Shape::kChunks + c) * Shape::kQBox, &tmQ, &bars.q_full, 64 * c, h0,
                           pl.q0 + tok0 + t * a.tokens);
           }
         }
-        int issued = 0;
         bool tail_pending = false;
         for (int i = 0; i < 2 * n_all; ++i) {
-          const int s = i % kSlots;
-          if (!warp_wait_converged(&bars.empty[s], ((i / kSlots) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) break;
+          const int s = static_cast<int>(loads % kSlots);
+          if (!warp_wait_converged(&bars.empty[s], ((loads / kSlots) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) break;
           const int row = (j0 + i / 2) * kTile;                 // first key of the tile, within the sequence
           const bool is_v = (i & 1) != 0;
           // value rows behind the sequence that are rows of the tensor (the
@@ -400,10 +427,10 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
               tma_load_3d(ring + s * Shape::kSlot + c * Shape::kBox, is_v ? &tmV : &tmK, bar, 64 * c, kh, pl.k0 + row);
           }
           __syncwarp();
-          ++issued;
-          if (cut) {   // at most once: the sequence's last tile
+          ++loads;
+          if (cut) {   // at most once a place: the sequence's last tile
             // the wait ignores the abort flag: the copy always lands
-            tail_pending = !warp_wait_converged(&bars.tail, 0, nullptr, a.status, a.wait_ns);
+            tail_pending = !warp_wait_converged(&bars.tail, tails++ & 1, nullptr, a.status, a.wait_ns);
             if (tail_pending) {
               *abort_flag = 1;
               break;
@@ -417,15 +444,16 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
             if (lane == 0) mbar_arrive(&bars.full[s]);
           }
         }
-        // every issued copy lands before the CTA exits
+        // every issued copy lands before the CTA exits or goes on
         if (lane == 0) {
-          (void)mbar_wait(&bars.q_full, 0, nullptr, nullptr, 100000000ull);
-          if (tail_pending) (void)mbar_wait(&bars.tail, 0, nullptr, nullptr, 100000000ull);
-          for (int s = 0; s < kSlots && s < issued; ++s) {
-            const int n_s = issued / kSlots + (s < issued % kSlots ? 1 : 0);
-            if (tail_pending && s == (issued - 1) % kSlots) continue;
-            (void)mbar_wait(&bars.full[s], static_cast<uint32_t>((n_s - 1) & 1), nullptr, nullptr, 100000000ull);
+          bool landed = mbar_wait(&bars.q_full, places_done & 1, nullptr, nullptr, 100000000ull);
+          if (tail_pending) landed &= mbar_wait(&bars.tail, (tails - 1) & 1, nullptr, nullptr, 100000000ull);
+          for (uint32_t s = 0; s < kSlots && s < loads; ++s) {
+            const uint32_t n_s = loads / kSlots + (s < loads % kSlots ? 1 : 0);
+            if (tail_pending && s == (loads - 1) % kSlots) continue;
+            landed &= mbar_wait(&bars.full[s], (n_s - 1) & 1, nullptr, nullptr, 100000000ull);
           }
+          if (!landed) *abort_flag = 1;
         }
         __syncwarp();
       }
@@ -443,25 +471,22 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
         auto score = [&](int t, uint32_t kt) {         // kt: the k tile's descriptor, lower half
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t step = (k / 4) * (Shape::kBox >> 4) + (k % 4) * 2;
-            const uint64_t qa = desc64(q_lo + t * (Shape::kChunks * Shape::kBox >> 4) + step, k_hi);
-            const uint64_t ka = desc64(kt + step, k_hi);
+            const uint64_t qa = desc64(q_lo + (t * Shape::kChunks + k / 4) * (Shape::kQBox >> 4) + (k % 4) * 2, k_hi);
+            const uint64_t ka = desc64(kt + (k / 4) * (Shape::kBox >> 4) + (k % 4) * 2, k_hi);
             if (k == 0) mma_ss<false>(el, tmem_base + Shape::s_col(t), qa, ka, idesc_s);
             else mma_ss<true>(el, tmem_base + Shape::s_col(t), qa, ka, idesc_s);
           }
           commit(el, &bars.s_full[t]);
         };
-        bool ok = warp_wait_converged<true>(&bars.q_full, 0, abort_flag, a.status, a.wait_ns) &&
-                  warp_wait_converged(&bars.full[0], 0, abort_flag, a.status, a.wait_ns);
+        bool ok = warp_wait_converged<true>(&bars.q_full, places_done & 1, abort_flag, a.status, a.wait_ns) &&
+                  warp_wait_converged(&bars.full[slot], phase, abort_flag, a.status, a.wait_ns);
         if (ok) {
           tc_fence_after();
 #pragma unroll
           for (int t = 0; t < NQ; ++t)
-            if (n[t] > 0) score(t, k_lo);
-          commit(el, &bars.empty[0]);
+            if (n[t] > 0) score(t, k_lo + slot * (Shape::kSlot >> 4));
+          commit(el, &bars.empty[slot]);
         }
-        int slot = 0;                                  // of the k tile last used
-        uint32_t phase = 0;
         auto next = [&] {
           if (++slot == kSlots) slot = 0, phase ^= 1;
         };
@@ -478,7 +503,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
             if (!ok || j >= n[t]) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              ok = ok && warp_wait_converged(half == 0 ? &bars.p_half[t] : &bars.p_full[t], j & 1, abort_flag, a.status, a.wait_ns);
+              ok = ok && warp_wait_converged(half == 0 ? &bars.p_half[t] : &bars.p_full[t], (tiles_done + j) & 1, abort_flag, a.status, a.wait_ns);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
@@ -505,7 +530,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
           }
         }
         commit(el, &bars.drain);
-        if (lane == 0) (void)mbar_wait(&bars.drain, 0, nullptr, nullptr, 100000000ull);
+        if (lane == 0 && !mbar_wait(&bars.drain, places_done & 1, nullptr, nullptr, 100000000ull)) *abort_flag = 1;
       }
       __syncwarp();
     } else {
@@ -532,7 +557,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
       const float c = a.scale_log2;
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
-        ok = warp_wait_converged(&bars.s_full[t], j & 1, abort_flag, a.status, a.wait_ns);
+        ok = warp_wait_converged(&bars.s_full[t], (tiles_done + j) & 1, abort_flag, a.status, a.wait_ns);
         if (!ok) break;
         tc_fence_after();
         uint32_t sv[4][32];
@@ -598,7 +623,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
         }
       }
       if (ok && nt > 0) {
-        ok = warp_wait_converged(&bars.o_full[t], 0, abort_flag, a.status, a.wait_ns);
+        ok = warp_wait_converged(&bars.o_full[t], places_done & 1, abort_flag, a.status, a.wait_ns);
         tc_fence_after();
       }
       if (ok) {
@@ -608,11 +633,12 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;            // no key seen: 0 (l is NaN for NaN scores)
         const float lse2 = l == 0.f ? -INFINITY : m + lg2(l);
         const int64_t row = static_cast<int64_t>(pl.q0) + tok;
+        const bool part = SPLIT && pl.nk > static_cast<int64_t>(a.chunk) * kTile;    // one of several chunks
         float* po = nullptr;
         uint16_t* out = nullptr;
         if (valid) {
           const int64_t at = row * a.Hq + head;
-          if (SPLIT) {
+          if (part) {
             const int64_t pat = static_cast<int64_t>(pl.chunk) * a.Tq * a.Hq + at;
             a.part_lse[pat] = lse2;
             po = a.part_o + pat * D;
@@ -631,7 +657,7 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
           if (valid) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(nt > 0 && l != 0.f ? __uint_as_float(o[i]) * inv : 0.f);
-            if (SPLIT) {
+            if (part) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 *reinterpret_cast<uint4*>(po + 32 * g + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
@@ -650,12 +676,21 @@ __global__ void __launch_bounds__((NQ * 4 + 2) * 32, NQ == 1 ? 2 : 1)
         }
       }
     }
+    if (!FEW || !SPLIT) break;
+    index += static_cast<int>(gridDim.x);
+    if (index >= a.blocks) break;
+    // copies have landed, MMAs are done and read: the next place may begin
+    if (n_all > 0) ++places_done, tiles_done += n_all;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag) break;
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, Shape::kTmemCols);
+    tmem_dealloc(bars.tmem_base, Shape::kTmemCols);
   }
 }
 
@@ -676,7 +711,8 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
   Place p{};
   if (!find_token(a, tok, p)) return;
   const int tiles = (p.nk + kTile - 1) / kTile;
-  const int chunks = max(1, (tiles + a.chunk - 1) / a.chunk);
+  const int chunks = (tiles + a.chunk - 1) / a.chunk;
+  if (chunks <= 1) return;                           // written already
   float top = -INFINITY;
   for (int c = lane; c < chunks; c += 32) top = fmaxf(top, a.part_lse[c * rows + w]);
 #pragma unroll
@@ -718,6 +754,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
 // workspace size is one too (148 SMs: a B200).
 struct Plan {
   int G, tokens, nq;
+  bool few;             // tiles of kFewRows rows
   int chunk;            // key tiles per chunk, 0: not split
   int64_t blocks;       // upper bound of (query tile, chunk) pairs over the sequences
   int64_t chunks;       // upper bound of chunks of one sequence
@@ -732,37 +769,45 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
   for (int d = 1; d <= kTile && d <= share; ++d)
     if (share % d == 0 && kTile / d * d >= 120) p.G = d;
   p.tokens = kTile / p.G;
+  p.few = p.G <= kFewRows && Tq <= B * (kFewRows / p.G);
+  if (p.few) p.tokens = kFewRows / p.G;
   const int64_t sets = Hq / p.G;
   const int64_t two = (Tq / (2 * p.tokens) + B) * sets;
   const int64_t one = (Tq / p.tokens + B) * sets;
   p.nq = Tq <= B * p.tokens || two < 148 ? 1 : 2;
   p.blocks = p.nq == 1 ? Tq / p.tokens + B : Tq / (2 * p.tokens) + B;
   p.chunks = 1;
-  if (p.nq == 1 && one < 296) {
+  const int64_t base = p.few ? B * sets : one;       // blocks of a call that is not split
+  if (p.nq == 1 && (p.few || base < 296)) {
     const int64_t tiles = (Tk + kTile - 1) / kTile, each = (tiles + B - 1) / B;
+    // Into how many chunks the keys of a sequence of `each` tiles go.
+    // Microseconds: a tile while each block has an SM, and else; to begin and
+    // end a block; for the join, and each chunk's part of it.  Few rows are
+    // bound by the keys' bytes (1 token x 32 / 8 heads over 131072 keys: 32
+    // tiles a chunk 88, 24 122, 8 107 us; 8 over 8192: 16 49, 8 53, 32 73; 4
+    // over 1000: 1 11.0, 4 13.9); tiles of many rows share the keys through L2
+    // (16384 queries x 1 head in two pieces 139 us, in one 210; 2048 x 8 heads
+    // in chunks of four tiles 44, in one piece 31).
+    const float alone = p.few ? 1.2f : 1.6f, beside = p.few ? 1.8f : 2.2f, ends = p.few ? 8.f : 5.f;
+    const float join = p.few ? 2.f : 4.f, piece = p.few ? 0.02f : Tq * Hq * 1.6e-4f;
     int64_t chunk = 0;
-    if (Tq <= B * p.tokens) {
-      // One query tile a sequence: the keys' bytes are the work.  About two
-      // rounds of two blocks per SM (8 tokens over 66796 keys: 58 us; one
-      // round 66, three 60, four 63), chunks of two tiles at least (1 token
-      // over 32768 keys: 14.4 us; of one 20.5, of four 15.2)
-      chunk = (tiles * one + B * 592 - 1) / (B * 592);
-      if (chunk < 2) chunk = 2;
-    } else {
-      // More than one: the keys are shared through L2.  Microseconds: 1.6 a
-      // tile while each block has an SM, else 2.2, 5 to begin and end a block;
-      // 4 for the join and the partial outputs twice through HBM.  In one
-      // piece and in two: 16384 queries x 1 head 210 us and 139, 2048 x 8
-      // heads 31 and 44 (chunks of four tiles)
-      float least = 0.f;
-      for (int64_t n = 1; n <= 16; ++n) {
-        const int64_t c = (each + n - 1) / n, blocks = one * n;
-        const float cost = ((blocks + 295) / 296) * (c * (blocks <= 148 ? 1.6f : 2.2f) + 5.f) +
-                           (n > 1 ? 4.f + n * Tq * Hq * 1.6e-4f : 0.f);
-        if (n == 1 || cost < least) least = cost, chunk = n == 1 ? 0 : c;
-      }
+    float least = 0.f;
+    for (int64_t n = 1; n <= 256 && n <= (each > 1 ? each : 1); n += n < 8 ? 1 : n / 4) {
+      const int64_t c = (each + n - 1) / n, blocks = base * n;
+      const float cost = ((blocks + 295) / 296) * (c * (blocks <= 148 ? alone : beside) + ends) +
+                         (n > 1 ? join + n * piece : 0.f);
+      if (n == 1 || cost < least) least = cost, chunk = n == 1 ? 0 : c;
     }
-    if (chunk != 0 && chunk * B < tiles) {
+    if (p.few) {
+      // Caches differ in length and the longest one ends last: where a join
+      // costs little beside the rest, what is twice the average is cut too (a
+      // cache of 32769 and 39 of 500: 70 us, whole 410; 64 of 2001: 96 and 88)
+      if (chunk == 0 && least > 30.f) chunk = 2 * each < 16 ? 16 : 2 * each;
+      // a workspace of at most 128 MB (at 128 columns)
+      const int64_t lines = Tq * Hq * 516, room = (int64_t(1) << 27) / lines;
+      if (chunk != 0 && chunk * room < tiles) chunk = room == 0 ? tiles : (tiles + room - 1) / room;
+    }
+    if (chunk != 0 && chunk < tiles && (p.few || chunk * B < tiles)) {
       p.chunk = static_cast<int>(chunk);
       const int64_t most = (Tq + p.tokens - 1) / p.tokens;      // query tiles of one sequence
       const int64_t x = most * (tiles / chunk + B), y = (Tq / p.tokens + B) * (tiles / chunk + 1);
@@ -792,11 +837,11 @@ int heads_map(CUtensorMap* map, const void* base, bool bf16, int64_t T, int64_t 
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <class T, int D, int NQ, bool SPLIT>
+template <class T, int D, int NQ, bool SPLIT, bool FEW>
 cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnArgs& a,
                       int64_t blocks, int64_t sets, int64_t chunks, cudaStream_t stream) {
-  using Shape = AttnShape<D, NQ>;
-  auto kernel = attention_tc_kernel<T, D, NQ, SPLIT>;
+  using Shape = AttnShape<D, NQ, FEW>;
+  auto kernel = attention_tc_kernel<T, D, NQ, SPLIT, FEW>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -810,7 +855,11 @@ cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUte
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(sets), 1);
+  // FEW and SPLIT, see the kernel: as many places as there are if a sequence's
+  // queries are one tile, two rounds of what the GPU holds at least
+  int64_t most = blocks;
+  if (FEW && SPLIT) most = std::max((592 + sets - 1) / sets, (static_cast<int64_t>(a.Tk) / kTile + 1) / a.chunk + a.B);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most), static_cast<unsigned>(sets), 1);
   cfg.blockDim = dim3(Shape::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Shape::kSmem;
   cfg.stream = stream;
@@ -824,9 +873,10 @@ cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUte
   const int64_t rows = static_cast<int64_t>(a.Tq) * a.Hq;
   cfg.blockDim = dim3(128, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  // chunks of one sequence at most.  A warp and four a row: 128 chunks of one
-  // token 34.5 us and 14.4 with the attention, two of 16384 139 us and 155
-  if (chunks > 8) {
+  // Four warps a row when a sequence may have many chunks and the rows fit the
+  // GPU at once: 128 chunks of one token 14.4 us with the attention, by a warp
+  // 34.5; two chunks of 16384 tokens 155 us and 139
+  if (chunks > 8 && rows <= 148 * 16) {
     cfg.gridDim = dim3(static_cast<unsigned>(rows), 1, 1);
     return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D, 4>, a);
   }
@@ -838,9 +888,14 @@ template <class T, int D>
 cudaError_t launch_plan(const Plan& p, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                         const AttnArgs& a, cudaStream_t stream) {
   const int64_t sets = a.Hq / p.G;
-  if (p.chunk != 0) return launch_tc<T, D, 1, true>(tmQ, tmK, tmV, a, p.blocks, sets, p.chunks, stream);
-  if (p.nq == 1) return launch_tc<T, D, 1, false>(tmQ, tmK, tmV, a, p.blocks, sets, p.chunks, stream);
-  return launch_tc<T, D, 2, false>(tmQ, tmK, tmV, a, p.blocks, sets, p.chunks, stream);
+  auto launch = [&](auto split, auto few) {
+    return launch_tc<T, D, 1, decltype(split)::value, decltype(few)::value>(tmQ, tmK, tmV, a, p.blocks, sets, p.chunks, stream);
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (p.few) return p.chunk != 0 ? launch(Yes{}, Yes{}) : launch(No{}, Yes{});
+  if (p.nq == 1) return p.chunk != 0 ? launch(Yes{}, No{}) : launch(No{}, No{});
+  return launch_tc<T, D, 2, false, false>(tmQ, tmK, tmV, a, p.blocks, sets, p.chunks, stream);
 }
 
 }  // namespace
@@ -853,6 +908,7 @@ extern "C" {
 // SPLIT: [chunks][Tq][Hq][D] fp32 partial outputs, [chunks][Tq][Hq] fp32 lse
 size_t w4a4_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
   if (Tq <= 0 || Tk < 0 || B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || D < 1) return 0;
+  if (Tq > (int64_t(1) << 30) || Tk > (int64_t(1) << 30) || B > (int64_t(1) << 24) || Hq > 65535 || D > 128) return 0;
   const Plan p = make_plan(Tq, Tk, B, Hq, Hk);
   if (p.chunk == 0) return 0;
   return static_cast<size_t>(p.chunks) * static_cast<size_t>(Tq) * static_cast<size_t>(Hq) * (D + 1) * 4;
@@ -899,6 +955,7 @@ int w4a4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
   a.causal = causal != 0;
   a.scale_log2 = scale * kLog2e;
   a.chunk = p.chunk;
+  a.blocks = static_cast<int>(p.blocks);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + (p.chunk != 0 ? p.chunks * Tq * Hq * D : 0);
   a.status = dev->status;
