@@ -241,6 +241,19 @@ def test_expired_waits_end_the_call(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M", [9, 12, 16, 25])
+@pytest.mark.parametrize("K,N", [(12288, 3001), (5120, 5000), (640, 9000), (9600, 33), (2080, 700)])
+@pytest.mark.parametrize("group,offset", [(32, True), (32, False), (128, True)])
+def test_every_split_of_more_rows(cuda_lib, M, K, N, group, offset):
+    """More than eight rows: 32 rows and 12 warps a CTA, or 16 and 8."""
+    if K % group:
+        group = 32
+    x, codes, scale, off, b = on_gpu(*make(M, K, N, group, torch.float16, offset, True, seed=N))
+    y = w4.linear_w4a16(x, codes, scale, offset=off, bias=b)
+    check(y, *[t.cpu() for t in reference(x, codes, scale, off, b)], K)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 2, 3, 8])
 @pytest.mark.parametrize("K,N", [(4096, 1000), (4096, 4090), (5120, 5000), (640, 9000), (1536, 2300), (9600, 33)])
 @pytest.mark.parametrize("group,offset", [(32, True), (64, False), (128, True)])

@@ -524,7 +524,19 @@ template <class T, int GROUP, bool OFFSET>
 cudaError_t launch_w16_rows(const W16Call& c, const W16Args& a) {
   if (a.M <= 2) return launch_w16_tiles<T, 1, true, GROUP, OFFSET>(c, a);
   if (a.M <= 8) return launch_w16_tiles<T, 1, false, GROUP, OFFSET>(c, a);
-  // more rows of x than weights per stage: two CTAs do not fit an SM
+  // More rows of x than weights per stage: two CTAs of 32 rows do not fit an
+  // SM.  One of 32 rows and 12 warps, or two of 16 rows and 8 warps, which read
+  // x twice as often, split k less and share an SM (a last round of one CTA per
+  // SM takes about half): microseconds of groups of 32, by their rounds.  Measured
+  // at 16 rows, groups of 128, 32 x 12 against 16 x 8: 4096->1024 7.4 and 4.8,
+  // 5120->5120 14.4 and 11.5, 2048->30000 30 and 24, 12288->3072 14.3 and 15.4;
+  // groups of 32: 5120->13824 25.3 and 27.0.
+  const int units = (a.K + kW16Cols - 1) / kW16Cols;
+  const int wide = (a.N + 31) / 32, narrow = (a.N + 15) / 16, pair = 2 * c.num_sms, rest = narrow % pair;
+  const float rounds = narrow / pair + (rest == 0 ? 0.f : rest <= c.num_sms ? 0.55f : 1.f);
+  if (0.5f + rounds * (0.9f + 1.55f * ((units + 7) / 8)) <
+      2.f + (wide + c.num_sms - 1) / c.num_sms * (0.7f + 1.8f * ((units + 11) / 12)))
+    return launch_w16<T, 1, 2, false, 8, GROUP, OFFSET>(c, a);
   return launch_w16<T, 2, 2, false, 12, GROUP, OFFSET>(c, a);
 }
 
