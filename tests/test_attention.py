@@ -148,6 +148,27 @@ def test_decoded_batches(cuda_lib, qs, ks, Hq, Hk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 64), (torch.float16, 128)], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("Hq,Hk", [(3, 1), (7, 1), (22, 2), (13, 1), (16, 1), (31, 1), (32, 1), (33, 1), (64, 1), (10, 2)])
+def test_decoded_head_groups(cuda_lib, dtype, D, Hq, Hk):
+    """Groups that fill 32 rows, leave some empty or do not fit them."""
+    go([1, 2, 0, 1, 3], [700, 2000, 5, 0, 129], Hq, Hk, D, dtype, True, seed=Hq)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 70, 900])
+def test_cache_past_32_bit_offsets(cuda_lib, n):
+    """The last sequence's keys lie behind 2^31 elements (4 GB) of k and v."""
+    ks, Hk, D = [2 ** 31 // (8 * 128) + 1000, 777], 8, 128
+    q = make(1 + n, 1, 16, 1, D, torch.bfloat16)[0]
+    k = torch.empty(sum(ks), Hk, D, device="cuda", dtype=torch.bfloat16).normal_()
+    v = torch.empty_like(k).normal_()
+    out, lse = w4.attention(q, k, v, cu([1, n]), cu(ks), causal=True, return_lse=True)
+    check(out[1:], lse[1:], q[1:], k[ks[0]:], v[ks[0]:], [n], [ks[1]], True)
+    assert torch.isfinite(out).all() and w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_expired_waits_of_a_decoded_batch(cuda_lib):
     q, k, v = make(64, 64 * 2000, 8, 1, 128, torch.bfloat16)
     cq, ck = cu([1] * 64), cu([2000] * 64)
