@@ -264,3 +264,15 @@ def test_every_split_of_rows_and_warps(cuda_lib, M, K, N, group, offset):
     y = w4.linear_w4a16(x, codes, scale, offset=off, bias=b)
     # the reference on the GPU, in float64
     check(y, *[t.cpu() for t in reference(x, codes, scale, off, b)], K)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 11])
+def test_weights_past_32_bit_offsets(cuda_lib, M):
+    """More than 2^31 bytes of codes: the last rows, and some before them."""
+    K, N, tail = 1024, 2 ** 31 // 512 + 1003, 2000
+    x, codes, scale, off, b = on_gpu(*make(M, K, tail, 128, torch.bfloat16, True, True))
+    far = lambda t: torch.cat((torch.zeros(N - tail, *t.shape[1:], device="cuda", dtype=t.dtype), t))
+    y = w4.linear_w4a16(x, far(codes), far(scale), offset=far(off), bias=far(b))
+    check(y[:, -tail:], *[t.cpu() for t in reference(x, codes, scale, off, b)], K)
+    assert (y[:, :-tail] == 0).all() and w4.last_device_error() == 0

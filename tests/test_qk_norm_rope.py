@@ -241,3 +241,19 @@ def test_binding_refusals(cuda_lib):
     for kind, call in bad:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_tokens_past_32_bit_offsets(cuda_lib, interleaved):
+    """More than 2^31 elements of q, whose last tokens come out as in a small call."""
+    T, H, D = 2 ** 31 // (8 * 64) + 77, 8, 64
+    q = torch.empty(T, H, D, device="cuda", dtype=torch.bfloat16).normal_()
+    _, _, w, _ = make(1, H, H, D, torch.bfloat16)
+    freq, axis = w4.rotary_frequencies((D,))
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    out, _ = w4.qk_norm_rope(q, None, w, None, pos, freq, axis, interleaved=interleaved)
+    last = slice(T - 100, T)
+    want, _ = w4.qk_norm_rope(q[last].clone(), None, w, None, pos[last].clone(), freq, axis, interleaved=interleaved)
+    check(want, reference(q[last], w, 1e-6, pos[last], freq, axis, interleaved))
+    assert torch.equal(out[last], want)
