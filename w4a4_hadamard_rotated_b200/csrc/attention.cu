@@ -42,7 +42,7 @@
 //     in shared memory and one softmax warp, and the ring holds a third k or v
 //     tile instead of the other 96 rows; the MMAs still run over 128 rows, those
 //     behind the 32 of whatever lies there and read by nobody (8 tokens over 66796
-//     keys: 50 us; with 128 rows, four warps and two tiles 58).
+//     keys: 51 us; with 128 rows, four warps and two tiles 58).
 // Measured (bf16, D 128, graph replays): 4608 x 24 heads 220 us, 1.18 PF/s;
 // 32760 x 10 heads 4.63 ms, 1.16 PF/s (the board's power limit holds the clock
 // at 1.75 GHz); eight causal prompts, 11168 tokens x 40/8 heads, fp16 381 us,
@@ -772,10 +772,16 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
   p.few = p.G <= kFewRows && Tq <= B * (kFewRows / p.G);
   if (p.few) p.tokens = kFewRows / p.G;
   const int64_t sets = Hq / p.G;
-  const int64_t two = (Tq / (2 * p.tokens) + B) * sets;
-  const int64_t one = (Tq / p.tokens + B) * sets;
+  // query tiles over the sequences at most: a sum of ceil(n / rows) over B
+  // parts of Tq, each part with one row at least
+  auto tiles_of = [&](int64_t rows) {
+    const int64_t t = (Tq + B * (rows - 1)) / rows;
+    return t < Tq ? t : Tq;
+  };
+  const int64_t two = tiles_of(2 * p.tokens) * sets;
+  const int64_t one = tiles_of(p.tokens) * sets;
   p.nq = Tq <= B * p.tokens || two < 148 ? 1 : 2;
-  p.blocks = p.nq == 1 ? Tq / p.tokens + B : Tq / (2 * p.tokens) + B;
+  p.blocks = tiles_of(p.nq * p.tokens);
   p.chunks = 1;
   const int64_t base = p.few ? B * sets : one;       // blocks of a call that is not split
   if (p.nq == 1 && (p.few || base < 296)) {
@@ -786,8 +792,8 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
     // bound by the keys' bytes (1 token x 32 / 8 heads over 131072 keys: 32
     // tiles a chunk 88, 24 122, 8 107 us; 8 over 8192: 16 49, 8 53, 32 73; 4
     // over 1000: 1 11.0, 4 13.9); tiles of many rows share the keys through L2
-    // (16384 queries x 1 head in two pieces 139 us, in one 210; 2048 x 8 heads
-    // in chunks of four tiles 44, in one piece 31).
+    // (16384 queries x 1 head in two pieces 130 us, in one 210; 2048 x 8 heads
+    // in chunks of four tiles 44, in one piece 29).
     const float alone = p.few ? 1.2f : 1.6f, beside = p.few ? 1.8f : 2.2f, ends = p.few ? 8.f : 5.f;
     const float join = p.few ? 2.f : 4.f, piece = p.few ? 0.02f : Tq * Hq * 1.6e-4f;
     int64_t chunk = 0;
@@ -810,7 +816,7 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
     if (chunk != 0 && chunk < tiles && (p.few || chunk * B < tiles)) {
       p.chunk = static_cast<int>(chunk);
       const int64_t most = (Tq + p.tokens - 1) / p.tokens;      // query tiles of one sequence
-      const int64_t x = most * (tiles / chunk + B), y = (Tq / p.tokens + B) * (tiles / chunk + 1);
+      const int64_t x = most * (tiles / chunk + B), y = tiles_of(p.tokens) * (tiles / chunk + 1);
       p.blocks = x < y ? x : y;
       p.chunks = (tiles + chunk - 1) / chunk;
     }
