@@ -128,3 +128,44 @@ def test_decoded_tokens_equal_the_prompt(cuda_lib):
         assert torch.equal(q1[0], qr[t]) and torch.equal(k1[0], kr[t])
         o, z = w4.attention(q1, kr[:t + 1], v[:t + 1], causal=True, return_lse=True)
         ta.check(o, z, q1, kr[:t + 1], v[:t + 1], [1], [t + 1], True)
+
+
+def test_small_layers_between_attentions(cuda_lib):
+    """Layers of a few rows (tensor memory of their own, the next kernel let in
+    early) between attentions that take all of an SM's tensor memory and those
+    that take half: a long chain without a gap, eager and replayed, ends and
+    gives what each call gives alone."""
+    block = Block(8, 8, seed=7)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)
+    long = [r(2600, 40, d) for d in (64, D)]                    # two query tiles a block
+    few = r(600, 2, 64)                                         # one, and chunks of keys
+    x = r(16, block.width)
+
+    def chain(times):
+        outs = []
+        for _ in range(times):
+            for t in (*long, few):
+                outs.append(w4.attention(t, t, t, causal=True))
+                outs.append(w4.linear_fused(x, *block.linears["out"]))
+        return outs
+
+    want = []
+    for t in (*long, few):
+        want.append(w4.attention(t, t, t, causal=True))
+        torch.cuda.synchronize()
+        want.append(w4.linear_fused(x, *block.linears["out"]))
+        torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(chain(20), want * 20))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain(1)                                                # the layers' workspace of this stream
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        outs = chain(5)
+    for _ in range(10):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want * 5)) and w4.last_device_error() == 0

@@ -202,11 +202,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 1) {
     tmem_alloc(&bars.tmem_base, kTmemCols);
     tmem_relinquish();
+    // A kernel launched after this one with programmatic stream serialization
+    // may start its own set-up now; it reads nothing this kernel writes before
+    // its grid-dependency wait, which returns only once this grid has finished.
+    // The CTA's first call counts, so it follows the allocation: a dependent that
+    // took tensor memory ahead of it (the attention kernel takes all of an SM's)
+    // would hold it until this grid ends, which waits for it.
+    griddep_launch_dependents();
   }
-  // A kernel launched after this one with programmatic stream serialization
-  // may start its own set-up now; it reads nothing this kernel writes before
-  // its grid-dependency wait, which returns only once this grid has finished.
-  griddep_launch_dependents();
   // launched with programmatic stream serialization: the set-up above may
   // overlap the previous kernel (the activation quantiser of a fused layer);
   // its outputs are read only after this point
