@@ -390,8 +390,9 @@ int w4a4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  *   D in {64, 128}; Hq % Hk == 0; 1 <= Hq <= 65535; 0 < scale <= 1e38;
  *   0 <= Tq, Tk <= 2^30, 1 <= B <= 2^24
  *   workspace: w4a4_attention_workspace_bytes(...) bytes of the same sizes
- *       (0 for most and for sizes that the call refuses), 256-byte aligned, no initialisation needed.  Calls that
- *       may overlap on the GPU need workspaces of their own.
+ *       (0 for most and for sizes that the call refuses, never more than
+ *       128 MiB), 256-byte aligned, no initialisation needed.  Calls that may
+ *       overlap on the GPU need workspaces of their own.
  * Key and value rows outside a query's sequence never reach it, whatever they
  * hold.  Inside a sequence a NaN or an infinity among the values may reach
  * queries that the causal rule keeps from seeing it (its weight 0 times the

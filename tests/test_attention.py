@@ -448,3 +448,34 @@ def test_expired_waits_end_the_call(cuda_lib):
     for c, g in zip(cases, good):
         assert torch.equal(w4.attention(*c, causal=True), g)
     assert w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 128), (torch.float16, 64)], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("qs,ks,H", [
+    ([590, 4, 3, 3], [8150, 20, 10, 12], 8),                                # one that has nearly all
+    ([3, 3, 4, 590], [12, 10, 20, 8150], 8),
+    ([1, 493, 0, 2, 1, 1, 1, 1], [5, 19950, 3, 0, 9, 11, 17, 5], 4),
+    ([150, 150, 150, 150], [2048, 2048, 2048, 2048], 8),                    # alike: most blocks have no place
+])
+def test_split_batches(cuda_lib, dtype, D, causal, qs, ks, H):
+    """Tiles of 128 rows whose keys are split, a block for every place there can be."""
+    go(qs, ks, H, H, D, dtype, causal, seed=qs[0])
+    assert sum(qs) > 32 * len(qs)
+
+
+@pytest.mark.gpu
+def test_batches_over_long_caches_take_little_memory(cuda_lib):
+    """More queries a sequence than a tile of few holds, over long caches: beside
+    the result the call takes 128 MB and a little."""
+    q, k, v = make(64 * 39, 64 * 8192, 8, 1, 128, torch.bfloat16)
+    c = [39] * 64, [8192] * 64
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    out, lse = w4.attention(q, k, v, cu(c[0]), cu(c[1]), causal=True, return_lse=True)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before <= 140 * 2 ** 20
+    check(out[-39:], lse[-39:], q[-39:], k[-8192:], v[-8192:], [39], [8192], True)
+    assert w4.last_device_error() == 0

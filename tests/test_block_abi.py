@@ -121,3 +121,12 @@ def test_rotary_frequencies():
     for bad in ((), (3,), (0, 4), (4, -2)):
         with pytest.raises(ValueError):
             w4.rotary_frequencies(bad)
+
+
+@pytest.mark.parametrize("Tq,Tk,B,Hq,Hk,D", [
+    (128 * 16, 128 * 32768, 128, 8, 1, 128), (128 * 128, 128 * 32768, 128, 1, 1, 128), (18 * 9, 18 * 16384, 18, 32, 8, 128),
+    (64 * 39, 64 * 8192, 64, 8, 1, 128), (64 * 33, 64 * 4096, 64, 8, 1, 128), (32 * 64, 32 * 8192, 32, 8, 1, 64),
+    (5 * 7, 5 * 2 ** 20, 5, 64, 8, 128), (2 ** 20, 2 ** 30, 2 ** 16, 1, 1, 128)])
+def test_attention_workspace_of_batches_stays_small(lib, Tq, Tk, B, Hq, Hk, D):
+    """The same for more queries a sequence than a tile of few holds."""
+    assert lib.w4a4_attention_workspace_bytes(Tq, Tk, B, Hq, Hk, D) <= 129 * 2 ** 20

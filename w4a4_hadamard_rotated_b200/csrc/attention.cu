@@ -795,13 +795,34 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
     // (16384 queries x 1 head in two pieces 130 us, in one 210; 2048 x 8 heads
     // in chunks of four tiles 44, in one piece 29).
     const float alone = p.few ? 1.2f : 1.6f, beside = p.few ? 1.8f : 2.2f, ends = p.few ? 8.f : 5.f;
-    const float join = p.few ? 2.f : 4.f, piece = p.few ? 0.02f : Tq * Hq * 1.6e-4f;
+    // Tiles of 128 rows get a block for each place there can be, and where the
+    // sequences are alike most of a batch's are none (64 x 39 queries x 8/1 heads
+    // over 8192 keys in chunks of 16 tiles: 768 of 49920): 6 ns each.
+    const float join = p.few ? 2.f : 4.f, piece = p.few ? 0.02f : Tq * Hq * 1.6e-4f, none = 0.006f;
+    // Upper bound of the (query tile, chunk) pairs of the sequences
+    auto places = [&](int64_t c) {
+      const int64_t most = (Tq + p.tokens - 1) / p.tokens;      // query tiles of one sequence
+      if (B == 1) return most * ((tiles + c - 1) / c);
+      return std::min(most * (tiles / c + B), tiles_of(p.tokens) * (tiles / c + 1));
+    };
+    // The workspace holds a line (516 bytes at 128 columns) for each row and each
+    // chunk of the longest sequence there can be, one with all the keys: at most
+    // 128 MB (128 x 16 queries x 8/1 heads over 32768 keys would take 7.5 GB
+    // beside 2.1 GB of keys and values)
+    const int64_t lines = Tq * Hq * 516, room = (int64_t(1) << 27) / lines;
+    const int64_t shortest = p.few ? 1 : room == 0 ? tiles : (tiles + room - 1) / room;
     int64_t chunk = 0;
     float least = 0.f;
     for (int64_t n = 1; n <= 256 && n <= (each > 1 ? each : 1); n += n < 8 ? 1 : n / 4) {
-      const int64_t c = (each + n - 1) / n, blocks = base * n;
-      const float cost = ((blocks + 295) / 296) * (c * (blocks <= 148 ? alone : beside) + ends) +
-                         (n > 1 ? join + n * piece : 0.f);
+      int64_t c = (each + n - 1) / n, pieces = n;
+      if (n > 1 && c < shortest) {
+        if (B == 1 || shortest >= each) break;      // one sequence: fewer pieces were looked at
+        c = shortest, pieces = (each + c - 1) / c;
+      }
+      const int64_t blocks = base * pieces;
+      float cost = ((blocks + 295) / 296) * (c * (blocks <= 148 ? alone : beside) + ends) +
+                   (n > 1 ? join + pieces * piece : 0.f);
+      if (!p.few && n > 1) cost += std::max<int64_t>(places(c) * sets - blocks, 0) * none;
       if (n == 1 || cost < least) least = cost, chunk = n == 1 ? 0 : c;
     }
     if (p.few) {
@@ -809,15 +830,11 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
       // costs little beside the rest, what is twice the average is cut too (a
       // cache of 32769 and 39 of 500: 70 us, whole 410; 64 of 2001: 96 and 88)
       if (chunk == 0 && least > 30.f) chunk = 2 * each < 16 ? 16 : 2 * each;
-      // a workspace of at most 128 MB (at 128 columns)
-      const int64_t lines = Tq * Hq * 516, room = (int64_t(1) << 27) / lines;
       if (chunk != 0 && chunk * room < tiles) chunk = room == 0 ? tiles : (tiles + room - 1) / room;
     }
     if (chunk != 0 && chunk < tiles && (p.few || chunk * B < tiles)) {
       p.chunk = static_cast<int>(chunk);
-      const int64_t most = (Tq + p.tokens - 1) / p.tokens;      // query tiles of one sequence
-      const int64_t x = most * (tiles / chunk + B), y = tiles_of(p.tokens) * (tiles / chunk + 1);
-      p.blocks = x < y ? x : y;
+      p.blocks = places(chunk);
       p.chunks = (tiles + chunk - 1) / chunk;
     }
   }
