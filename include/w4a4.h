@@ -376,7 +376,10 @@ int w4a4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  * s_j = scale * q_i . k_j over the keys it sees and head h reading key head
  * h / (Hq / Hk):
  *     lse = log sum_j exp(s_j),   out = round16( sum_j exp(s_j - lse) v_j )
- * A query that sees nothing gets out = 0 and lse = -inf.  The pages have no
+ * A query that sees nothing gets out = 0 and lse = -inf.  Scores, weights, sums
+ * and lse are fp32, but each weight is rounded to dtype before it meets v_j (the
+ * tensor cores' operand type): half a step relative to the weight, and in fp16
+ * at most 2^-36 of the largest weight, where that is more.  The pages have no
  * counterpart to this entry point.
  *   q [Tq, Hq, D], k [Tk, Hk, D], v [Tk, Hk, D] dtype; token and head strides
  *       in elements, multiples of 8, 16-byte aligned, D contiguous

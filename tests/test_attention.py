@@ -479,3 +479,32 @@ def test_batches_over_long_caches_take_little_memory(cuda_lib):
     assert torch.cuda.max_memory_allocated() - before <= 140 * 2 ** 20
     check(out[-39:], lse[-39:], q[-39:], k[-8192:], v[-8192:], [39], [8192], True)
     assert w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("rows,keys,H", [(300, 4096, 2), (1, 4096, 2), (2600, 4096, 40), (200, 2 ** 17, 1), (40, 500, 3)])
+@pytest.mark.parametrize("at", [0, 77, 130, -1])
+def test_many_small_weights_beside_one_large(cuda_lib, dtype, rows, keys, H, at):
+    """One key that takes nearly all of the softmax and has value 0, and keys
+    17.6875 below it (2^-25.5 of its weight) with value 1: the result is their
+    whole share.  Scores are one product and exact, as are the scale of 1 and
+    18 ln 2's place in fp32 to 2^-24 relative: weights off by 2^-18 with the
+    exponential's 2^-22; sums of L terms L 2^-23; weights rounded to 16 bits by
+    half a step, eps/2, and in fp16 (which holds them times 2^11 or more) by at
+    most 2^-36 of the largest each; the output by half a step, in fp16 2^-25 at least."""
+    D = 64
+    q = torch.zeros(rows, H, D, device="cuda", dtype=dtype)
+    k = torch.zeros(keys, H, D, device="cuda", dtype=dtype)
+    v = torch.ones(keys, H, D, device="cuda", dtype=dtype)
+    q[..., 3] = 1
+    k[..., 3] = 0.3125
+    k[at, :, 3], v[at] = 18, 0
+    out, lse = w4.attention(q, k, v, scale=1.0, return_lse=True)
+    small = (keys - 1) * math.exp(-17.6875)
+    want, eps = small / (1 + small), torch.finfo(dtype).eps
+    tol = want * (eps + 2.0 ** -18 + keys * 2.0 ** -23) + 2.0 ** -25
+    if dtype == torch.float16:
+        tol += keys * 2.0 ** -36
+    assert (out.double() - want).abs().max() <= tol
+    assert (lse.double() - 18 - math.log1p(small)).abs().max() <= 19 * 2.0 ** -20 + keys * 2.0 ** -23

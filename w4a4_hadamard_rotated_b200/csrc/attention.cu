@@ -28,9 +28,14 @@
 //     read, and a commit of S(j + 1) tells that O(j) is complete: the softmax
 //     warps rescale O themselves, no further role and no further barrier.
 //   * The maximum in use follows the running one only when it falls behind
-//     by more than 8 (in log2 units): weights stay below 2^8 and the rescaling
-//     of O, a round trip through tensor memory, becomes rare.  The result is
-//     the same quotient.
+//     by more than 8 (fp16: 4, in log2 units), so that the rescaling of O, a
+//     round trip through tensor memory, becomes rare.  The result is the same
+//     quotient.
+//   * In fp16 all weights and sums are 2^11 times as large (at most 2^15 with
+//     what the maximum may be behind; fp16 holds 2^16), or keys 2^-14 below the
+//     largest would already be subnormal and those 2^-25 below it nothing, while
+//     the sum counts them in full: 4095 of them behind one whose value is 0 came
+//     out 86% too small.  Now that begins at 2^-25 and 2^-36.
 //   * Masks select (-inf) rather than add, on the tiles they cut only.  Value
 //     rows behind a sequence's end inside its last tile are zeroed in
 //     shared memory, so whatever lies there reaches nothing.
@@ -69,7 +74,12 @@ constexpr int kTile = 128;             // query rows per MMA tile and keys per k
 constexpr int kFewRows = 32;           // query rows of a tile of few
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescale = 8.f;        // how far (log2) the maximum in use may fall behind
+// log2: how far the maximum in use may fall behind, and how far below it the
+// weights' unit lies
+template <class T>
+constexpr float kBehind = std::is_same<T, Bf16>::value ? 8.f : 4.f;
+template <class T>
+constexpr float kUnit = std::is_same<T, Bf16>::value ? 0.f : 11.f;
 
 struct AttnArgs {
   uint16_t* out;
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(AttnShape<D, NQ, FEW>::kThreads, NQ == 1 ? 2 :
       seen -= j0 * kTile;
       fewest -= j0 * kTile;
       const int nt = n[t];
-      float m = -INFINITY;                           // the maximum in use, times scale_log2
+      float m = -INFINITY;                           // the score of weight 1, times scale_log2: the maximum in use less kUnit
       uint64_t l2[2] = {0, 0};                       // partial sums (four fp32)
       const float c = a.scale_log2;
       bool ok = true;
@@ -580,12 +590,12 @@ __global__ void __launch_bounds__(AttnShape<D, NQ, FEW>::kThreads, NQ == 1 ? 2 :
         }
         const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], __uint_as_float(sv[0][31]), __uint_as_float(sv[1][31])),
                                max3(__uint_as_float(sv[2][31]), __uint_as_float(sv[3][31]), -INFINITY)) * c;
-        const bool behind = top - m > kRescale;      // false for -inf - -inf
+        const bool behind = top - m > kBehind<T> + kUnit<T>;     // false for -inf - -inf
         if (j == 0) {
-          if (behind) m = top;
+          if (behind) m = top - kUnit<T>;
         } else if (__any_sync(0xFFFFFFFFu, behind)) {
-          const float f = behind ? ex2(m - top) : 1.f;
-          if (behind) m = top;
+          const float f = behind ? ex2(m - (top - kUnit<T>)) : 1.f;
+          if (behind) m = top - kUnit<T>;
           const uint64_t ff = pack2(f, f);
           const uint64_t zero = 0;
           l2[0] = fma2(l2[0], ff, zero);
