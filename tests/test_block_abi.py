@@ -3,6 +3,9 @@ arguments come back as status codes before any CUDA call, and the binding
 refuses tensors the library cannot take."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -130,3 +133,39 @@ def test_rotary_frequencies():
 def test_attention_workspace_of_batches_stays_small(lib, Tq, Tk, B, Hq, Hk, D):
     """The same for more queries a sequence than a tile of few holds."""
     assert lib.w4a4_attention_workspace_bytes(Tq, Tk, B, Hq, Hk, D) <= 129 * 2 ** 20
+
+
+def run_copy(tmp_path, leave_out, code):
+    """`code` in a fresh interpreter over a copy of the package without some of its files."""
+    at = tmp_path / "w4a4_hadamard_rotated_b200"
+    at.mkdir()
+    here = os.path.dirname(w4.__file__)
+    for name in ("__init__.py", "libw4a4.so", "_binding.so"):
+        if name not in leave_out:
+            os.symlink(os.path.join(here, name), at / name)
+    code = f"import sys; sys.path.insert(0, {str(tmp_path)!r})\nimport torch, w4a4_hadamard_rotated_b200 as w4\n" + code
+    return subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=tmp_path)
+
+
+def test_layer_entries_do_not_need_the_extension(tmp_path):
+    """libw4a4.so alone serves every entry but the three that the extension
+    marshals, and those say what is missing."""
+    r = run_copy(tmp_path, ["_binding.so"], """
+assert w4.load_library().w4a4_version() >= 100
+assert w4.linear_kernel(4096, 512, 512) == 0
+h = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+for call in (lambda: w4.linear(h, h, h, h), lambda: w4.quantize_weight_w4a16(h)):
+    try:
+        call()
+        raise SystemExit("taken")
+    except TypeError:
+        pass
+for call in (lambda: w4.attention(h, h, h), lambda: w4.qk_norm_rope(h, h), lambda: w4.linear_w4a16(h, h, h)):
+    for _ in range(2):
+        try:
+            call()
+            raise SystemExit("taken")
+        except RuntimeError as e:
+            assert "_binding.so is missing" in str(e), e
+""")
+    assert r.returncode == 0, r.stdout + r.stderr

@@ -5,8 +5,8 @@ next to this file).  The binding only marshals arguments: it checks tensor
 dtypes, devices and layouts, allocates outputs with PyTorch, and passes raw
 device pointers plus the current CUDA stream to the library (ctypes here; for
 the entries that run between a block's linears, whose calls are short and
-have many arguments, in the extension _binding.so).  Every step of the layer runs in the library's CUDA kernels; there is no CPU or PyTorch
-fallback, and every call raises if the library is missing or not built.
+have many arguments, in the extension _binding.so).  Every step of the layer
+runs in the library's CUDA kernels; there is no CPU or PyTorch fallback, and every call raises if what it needs is missing or not built.
 
 Functions keep the C names without the ``w4a4_`` prefix:
   quantize_weight(W, g)                      -> (Wq [N, K/2] int8, sw [N] fp32)
@@ -86,25 +86,24 @@ class W4A4Error(RuntimeError):
         super().__init__(f"{what}: {name}")
 
 
+def _need_built(path):
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build() "
+                           "(or python w4a4_hadamard_rotated_b200/build.py)")
+
+
 def load_library(path=LIB_PATH):
-    """Load libw4a4.so (once), declare its C signatures and hand the block
-    entries' addresses to _binding.so."""
-    global _lib, _native
+    """Load libw4a4.so (once) and declare its C signatures."""
+    global _lib
     if _lib is not None:
         return _lib
-    for needed in (path, os.path.join(_HERE, "_binding.so")):
-        if not os.path.exists(needed):
-            raise RuntimeError(f"{needed} is missing: build it with __graft_entry__.build() "
-                               "(or python w4a4_hadamard_rotated_b200/build.py)")
+    _need_built(path)
     lib = ctypes.CDLL(path)
     for name, (res, args) in SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    from . import _binding
-    _binding.bind(W4A4Error, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-        "w4a4_linear_w4a16", "w4a4_qk_norm_rope", "w4a4_attention", "w4a4_attention_workspace_bytes")))
-    _lib, _native = lib, _binding
+    _lib = lib
     return lib
 
 
@@ -387,7 +386,16 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1}      # W4A4_BF16, W4A4_FP16
 
 
 def _bound():
-    load_library()
+    """_binding.so with the library's entry points, loaded at the first of the
+    three calls that go through it: the other entries need libw4a4.so alone."""
+    global _native
+    if _native is None:
+        lib = load_library()
+        _need_built(os.path.join(_HERE, "_binding.so"))
+        from . import _binding
+        _binding.bind(W4A4Error, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "w4a4_linear_w4a16", "w4a4_qk_norm_rope", "w4a4_attention", "w4a4_attention_workspace_bytes")))
+        _native = _binding
     return _native
 
 
