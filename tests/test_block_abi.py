@@ -140,7 +140,7 @@ def run_copy(tmp_path, leave_out, code):
     at = tmp_path / "w4a4_hadamard_rotated_b200"
     at.mkdir()
     here = os.path.dirname(w4.__file__)
-    for name in ("__init__.py", "libw4a4.so", "_binding.so"):
+    for name in ("__init__.py", "build.py", "libw4a4.so", "_binding.so"):
         if name not in leave_out:
             os.symlink(os.path.join(here, name), at / name)
     code = f"import sys; sys.path.insert(0, {str(tmp_path)!r})\nimport torch, w4a4_hadamard_rotated_b200 as w4\n" + code
@@ -169,3 +169,35 @@ for call in (lambda: w4.attention(h, h, h), lambda: w4.qk_norm_rope(h, h), lambd
             assert "_binding.so is missing" in str(e), e
 """)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_extension_of_another_pytorch_or_python_is_not_loaded(tmp_path):
+    r = run_copy(tmp_path, [], """
+h = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+torch.__version__ = "1.0"
+try:
+    w4.attention(h, h, h)
+    raise SystemExit("taken")
+except RuntimeError as e:
+    assert "not built for torch 1.0" in str(e), e
+assert w4.load_library().w4a4_version() >= 100
+""")
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_extension_is_built_again_for_another_pytorch(monkeypatch):
+    """By the build's rule of what is up to date; the compiler is not run."""
+    from w4a4_hadamard_rotated_b200 import build
+    ran = []
+
+    def run(cmd, **_):
+        ran.append(cmd)
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    monkeypatch.setattr(build, "_up_to_date", lambda *_: True)     # by its time
+    build.build_binding()
+    assert not ran
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    build.build_binding()
+    assert len(ran) == 1 and any("torch 1.0" in a for a in ran[0])

@@ -391,7 +391,12 @@ def _bound():
     global _native
     if _native is None:
         lib = load_library()
-        _need_built(os.path.join(_HERE, "_binding.so"))
+        path = os.path.join(_HERE, "_binding.so")
+        _need_built(path)
+        from . import build
+        if not build._built_for_this(path):
+            raise RuntimeError(f"{path} was not built for {build.built_for()}: build it again with "
+                               "__graft_entry__.build() (or python w4a4_hadamard_rotated_b200/build.py)")
         from . import _binding
         _binding.bind(W4A4Error, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "w4a4_linear_w4a16", "w4a4_qk_norm_rope", "w4a4_attention", "w4a4_attention_workspace_bytes")))

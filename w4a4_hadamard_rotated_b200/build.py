@@ -45,6 +45,19 @@ def _up_to_date(obj, deps):
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def built_for():
+    """What _binding.so is tied to: it links PyTorch's and Python's internals."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def _built_for_this(lib):
+    """Whether the extension at `lib` was compiled for this PyTorch and Python
+    (the text is in it; one for others is not loaded to ask it)."""
+    with open(lib, "rb") as f:
+        return f"built for <{built_for()}>".encode() in f.read()
+
+
 def build_binding(force=False):
     """_binding.so: the marshalling of the block entries."""
     import sysconfig
@@ -52,11 +65,12 @@ def build_binding(force=False):
     import torch
 
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and _up_to_date(BINDING, [src, os.path.join(INCLUDE, "w4a4.h")]):
+    if not force and _up_to_date(BINDING, [src, os.path.join(INCLUDE, "w4a4.h")]) and _built_for_this(BINDING):
         return BINDING
     root = os.path.dirname(torch.__file__)
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DBUILT_FOR="built for <{built_for()}>"', "-I", INCLUDE,
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"],

@@ -345,7 +345,9 @@ PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// The documentation names what the extension was compiled for (BUILT_FOR comes
+// from build.py, which looks for it in the file before it loads or keeps it).
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", BUILT_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
