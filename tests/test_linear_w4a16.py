@@ -276,3 +276,27 @@ def test_weights_past_32_bit_offsets(cuda_lib, M):
     y = w4.linear_w4a16(x, far(codes), far(scale), offset=far(off), bias=far(b))
     check(y[:, -tail:], *[t.cpu() for t in reference(x, codes, scale, off, b)], K)
     assert (y[:, :-tail] == 0).all() and w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 5, 16])
+def test_expired_waits_are_reported(cuda_lib, M):
+    """Weights of 77 MB that are not in L2: some warp has to wait for a stage,
+    and with a limit of a few nanoseconds it gives up and says so. The call after it is right."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    K, N = 5120, 30000
+    codes = torch.randint(-128, 128, (N, K // 2), generator=gen, device="cuda", dtype=torch.int8)
+    scale = torch.full((N, K // 64), 0.01, device="cuda", dtype=torch.bfloat16)
+    x = torch.randn(M, K, generator=gen, device="cuda").to(torch.bfloat16)
+    good = w4.linear_w4a16(x, codes, scale)
+    cold = torch.empty(2 ** 28, device="cuda", dtype=torch.uint8)
+    w4.debug_set_wait_limit(5)
+    try:
+        for i in range(3):
+            cold.fill_(i)
+            torch.cuda.synchronize()
+            w4.linear_w4a16(x, codes, scale)
+            assert w4.last_device_error() == 8
+    finally:
+        w4.debug_set_wait_limit(0)
+    assert torch.equal(w4.linear_w4a16(x, codes, scale), good) and w4.last_device_error() == 0
