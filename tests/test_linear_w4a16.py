@@ -300,3 +300,47 @@ def test_expired_waits_are_reported(cuda_lib, M):
     finally:
         w4.debug_set_wait_limit(0)
     assert torch.equal(w4.linear_w4a16(x, codes, scale), good) and w4.last_device_error() == 0
+
+
+def slice_edges(K):
+    """Columns beside the ends of the slices of k that 8, 12 and 16 warps take, in steps of 128."""
+    units, cols = (K + 127) // 128, set()
+    for warps in (8, 12, 16):
+        for w in range(warps + 1):
+            end = min(units * w // warps * 128, K)
+            cols |= set(range(max(end - 32, 0), min(end + 32, K)))
+    return sorted(cols)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("M", [1, 2, 5, 8, 16, 20])
+@pytest.mark.parametrize("K,N", [(32, 5), (96, 33), (640, 9000), (1984, 257), (2080, 700), (4096, 1000), (5120, 5000),
+                                 (9600, 33), (12288, 3001), (131072, 9)])
+def test_whole_numbers_are_exact(cuda_lib, dtype, M, K, N):
+    """Small whole x, scales 1/2, 1 and 2, offsets that are multiples of 1/2:
+    every product and partial sum is a multiple of 1/2 below 2^23 (K (2 * 8 * 2 +
+    2 * 2) <= 36 * 2^17 for the longest row), which fp32 holds, so the result is the exact sum
+    rounded once. With x everywhere, with x beside the ends of the warps' slices
+    only, and with x in the last 32 columns only: a column lost, read twice or
+    met with another group's scale shows."""
+    gen = torch.Generator(device="cuda").manual_seed(K + N + M)
+    r = lambda lo, hi, *s: torch.randint(lo, hi + 1, s, generator=gen, device="cuda")
+    codes = r(-128, 127, N, K // 2).to(torch.int8)
+    bias = r(-8, 8, N).to(dtype)
+    for group, offset in ((32, True), (32, False), (64, False), (64, True), (128, True), (128, False)):
+        if K % group:
+            continue
+        scale = torch.tensor([0.5, 1.0, 2.0], device="cuda")[r(0, 2, N, K // group)].to(dtype)
+        off = (r(-4, 4, N, K // group) * 0.5).to(dtype) if offset else None
+        w = unpack(codes) * scale.double().repeat_interleave(group, 1)
+        if offset:
+            w += off.double().repeat_interleave(group, 1)
+        for where in (range(K), slice_edges(K), range(K - 32, K)):
+            x = torch.zeros(M, K, device="cuda", dtype=dtype)
+            at = torch.tensor(list(where), device="cuda")
+            x[:, at] = r(-2, 2, M, len(at)).to(dtype)
+            y = w4.linear_w4a16(x, codes, scale, offset=off, bias=bias)
+            want = x.double() @ w.t() + bias.double()
+            assert torch.equal(y, want.to(dtype)), (group, offset, len(at))
+    assert w4.last_device_error() == 0
