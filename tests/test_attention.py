@@ -508,3 +508,108 @@ def test_many_small_weights_beside_one_large(cuda_lib, dtype, rows, keys, H, at)
         tol += keys * 2.0 ** -36
     assert (out.double() - want).abs().max() <= tol
     assert (lse.double() - 18 - math.log1p(small)).abs().max() <= 19 * 2.0 ** -20 + keys * 2.0 ** -23
+
+
+SENSITIVE = [
+    ([700, 1, 260], [3000, 900, 2100], 6, 2),
+    ([1] * 5, [20000, 1, 129, 8192, 777], 32, 8),
+    ([1100], [1100], 40, 40),
+    ([300], [6000], 1, 1),
+    ([1, 0, 4, 2, 1] * 8, [300, 70, 1500, 0, 2600] * 8, 8, 1),
+    ([1025, 130, 1, 257, 0, 700], [1025, 130, 1, 257, 0, 700], 40, 8),
+    ([40, 33], [20000, 300], 8, 1),
+    ([590, 4, 3, 3], [8150, 20, 10, 12], 8, 8),
+    ([2, 300, 5], [127, 40, 256], 4, 2),
+]
+
+
+def seen_by(n, m, causal):
+    """[n, m]: whether query i sees key j."""
+    i, j = torch.arange(n, device="cuda")[:, None], torch.arange(m, device="cuda")
+    return j <= i + (m - n) if causal else torch.ones(n, m, dtype=torch.bool, device="cuda")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("qs,ks,Hq,Hk", SENSITIVE)
+def test_every_key_counts_once(cuda_lib, dtype, D, causal, qs, ks, Hq, Hk):
+    """Queries of zeros: all weights are alike and exact, and so are their sums.
+    The keys at the ends of tiles and sequences have value 1 in a column of their
+    own or one that they share with a few, so the result is a small count over
+    the number of keys seen: one lost or counted twice moves it by several
+    percent, a bad bound of the keys moves lse.
+    Bounds: the output's rounding, eps/2 (in fp16 2^-25 at least); the quotient
+    and the join of chunks: some roundings, exponentials and logarithms of 2^-22
+    to 2^-21 absolute, 2^-18 together, and 2^-19 (1 + |lse|) for lse."""
+    rows = 30                                                    # behind the last sequence
+    q = torch.zeros(sum(qs), Hq, D, device="cuda", dtype=dtype)
+    k = make(1, sum(ks) + rows, 1, Hk, D, dtype)[1]
+    v = torch.zeros(sum(ks) + rows, Hk, D, device="cuda", dtype=dtype)
+    v[sum(ks):] = 1
+    at = 0
+    for m in ks:
+        edge = [j for j in range(m) if j % 128 in (0, 1, 126, 127) or j >= m - 3]
+        v[at + torch.tensor(edge, dtype=torch.long), :, torch.arange(len(edge)) % D] = 1
+        at += m
+    out, lse = w4.attention(q, k, v, cu(qs), cu(ks), causal=causal, return_lse=True)
+    q0 = k0 = 0
+    for n, m in zip(qs, ks):
+        seen = seen_by(n, m, causal).double()
+        total = seen.sum(1)
+        want = (seen @ v[k0:k0 + m].double().flatten(1)).view(n, Hk, D) / total.clamp(min=1)[:, None, None]
+        want = want.repeat_interleave(Hq // Hk, 1)
+        tol = want * (torch.finfo(dtype).eps / 2 + 2.0 ** -18) + (2.0 ** -25 if dtype == torch.float16 else 0)
+        assert ((out[q0:q0 + n].double() - want).abs() <= tol).all()
+        z, off = total.log()[:, None], lse[q0:q0 + n].double()
+        assert torch.where(z == -math.inf, off == z, (off - z).abs() <= 2.0 ** -19 * (1 + z.abs())).all()
+        q0, k0 = q0 + n, k0 + m
+    assert w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("qs,ks,Hq,Hk", SENSITIVE)
+def test_one_key_takes_all(cuda_lib, dtype, D, causal, qs, ks, Hq, Hk):
+    """Each key head of a sequence has one key whose score lies 100 or more above
+    the others', at the edges of tiles, chunks and the sequence in turn: the
+    result is its value, bit for bit (all other weights are nothing). Keys of the
+    next sequence and those behind the last score higher still, so that one
+    reached by mistake would take all."""
+    rows, ends = 30, [0]
+    for m in ks:
+        ends.append(ends[-1] + m)
+    gen = torch.Generator().manual_seed(sum(ks) + D)
+    q = make(sum(qs), 1, Hq, 1, D, dtype)[0] * 0
+    q[..., 5] = 1
+    _, k, v = make(1, ends[-1] + rows, 1, Hk, D, dtype, seed=3)
+    for turn in range(4):
+        k[..., 5] = k[..., 5].clamp(-4, 4)
+        k[ends[-1]:, :, 5] = 960
+        where, score = {}, {}
+        for b, m in enumerate(ks):
+            edge = sorted({j for j in (0, 1, 127, 128, 129, 255, 256, m // 2, m - 129, m - 128, m - 127, m - 2, m - 1)
+                           if 0 <= j < m})
+            edge += [j for j in torch.randint(0, max(m // 128, 1), (4,), generator=gen).mul(128).tolist() if j < m]
+            for h in range(Hk):
+                if edge:
+                    where[b, h] = edge[(h + 5 * b + turn * (Hk + 1)) % len(edge)]
+                    score[b] = 128 + 16 * b
+                    k[ends[b] + where[b, h], h, 5] = score[b]
+        out, lse = w4.attention(q, k, v, cu(qs), cu(ks), causal=causal, scale=1.0, return_lse=True)
+        q0 = 0
+        for b, (n, m) in enumerate(zip(qs, ks)):
+            for h in range(Hk):
+                if (b, h) not in where or n == 0:
+                    continue
+                j, G = where[b, h], Hq // Hk
+                rows_seeing = seen_by(n, m, causal)[:, j]
+                got = out[q0:q0 + n, h * G:(h + 1) * G][rows_seeing]
+                assert torch.equal(got, v[ends[b] + j, h].expand_as(got)), (turn, b, h, j)
+                z = lse[q0:q0 + n, h * G:(h + 1) * G][rows_seeing].double()
+                assert ((z - score[b]).abs() <= 2.0 ** -19 * (1 + score[b])).all()
+            q0 += n
+    assert w4.last_device_error() == 0
