@@ -390,6 +390,9 @@ int w4a4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  *       bad array reads and writes nothing out of range); both NULL with
  *       B == 1: one sequence of all the rows
  *   Rows of out and lse behind the last sequence keep what they hold.
+ *   Caches with room to grow need no repacking: a sequence without queries
+ *       stands for the unused rows behind each (B is then twice their number),
+ *       whatever those hold
  *   D in {64, 128}; Hq % Hk == 0; 1 <= Hq <= 65535; 0 < scale <= 1e38;
  *   0 <= Tq, Tk <= 2^30, 1 <= B <= 2^24
  *   workspace: w4a4_attention_workspace_bytes(...) bytes of the same sizes

@@ -613,3 +613,42 @@ def test_one_key_takes_all(cuda_lib, dtype, D, causal, qs, ks, Hq, Hk):
                 assert ((z - score[b]).abs() <= 2.0 ** -19 * (1 + score[b])).all()
             q0 += n
     assert w4.last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D,Hq,Hk", [(torch.bfloat16, 128, 32, 8), (torch.float16, 64, 8, 1)], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("n", [1, 7])
+def test_caches_with_room_to_grow(cuda_lib, dtype, D, Hq, Hk, n):
+    """One buffer of 5 caches of 3000 rows, of which some are filled: sequences
+    without queries stand for the rest of each, whatever it holds. The same
+    buffer and lengths that grow on the device, replayed from a graph."""
+    B, room = 5, 3000
+    used = [2999, 130, n, 3000, 1024]
+    q, k, v = make(B * n, B * room, Hq, Hk, D, dtype)
+    filled = torch.zeros(B, room, dtype=torch.bool, device="cuda")
+
+    def lengths():
+        at = [(room * b, room * b + m) for b, m in enumerate(used)]
+        return torch.tensor([x for pair in at for x in pair] + [B * room], dtype=torch.int32, device="cuda")
+
+    cq = torch.tensor([n * ((i + 1) // 2) for i in range(2 * B + 1)], dtype=torch.int32, device="cuda")
+    ck = lengths()
+    g = torch.cuda.CUDAGraph()
+    w4.attention(q, k, v, cq, ck, causal=True)
+    with torch.cuda.graph(g):
+        out, lse = w4.attention(q, k, v, cq, ck, causal=True, return_lse=True)
+    for _ in range(3):
+        filled[:] = False
+        for b, m in enumerate(used):
+            filled[b, :m] = True
+        rest = ~filled.view(-1)
+        ck.copy_(lengths())
+        k[rest], v[rest] = math.nan, math.inf
+        g.replay()
+        check(out, lse, q, k[~rest], v[~rest], [n] * B, used, True)
+        assert torch.isfinite(out).all() and w4.last_device_error() == 0
+        # each cache takes a token more, where it has room
+        for b in range(B):
+            if used[b] < room:
+                k[room * b + used[b]], v[room * b + used[b]] = q[b, :Hk], 1
+                used[b] += 1

@@ -467,11 +467,14 @@ def attention(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, causal=False, scale
     fp32) with return_lse.
       cu_seqlens_q, cu_seqlens_k [B + 1] int32 on the device: where each
         packed sequence begins among the query and the key rows; both None:
-        one sequence
+        one sequence.  Caches with room to grow lie as they are: a sequence
+        without queries stands for the unused rows behind each
       causal: query i of a sequence sees keys j <= i + Lk - Lq
       scale: 1/sqrt(D) unless given
-    Rows behind the last sequence keep what `out` held (a new `out` holds
-    nothing defined there); queries that see no key get 0 and lse -inf."""
+    Each weight of the softmax is rounded to q's type before it meets v (scores
+    and sums are fp32).  `out` may not overlap q, k or v.  Rows behind the last
+    sequence keep what `out` held (a new `out` holds nothing defined there);
+    queries that see no key get 0 and lse -inf."""
     return (_native or _bound()).attention(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out, return_lse)
 
 
