@@ -394,7 +394,7 @@ int w4a4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  *       stands for the unused rows behind each (B is then twice their number),
  *       whatever those hold
  *   D in {64, 128}; Hq % Hk == 0; 1 <= Hq <= 65535; 0 < scale <= 1e38;
- *   0 <= Tq, Tk <= 2^30, 1 <= B <= 2^24
+ *   0 <= Tq, Tk <= 2^30, 1 <= B <= 65536
  *   workspace: w4a4_attention_workspace_bytes(...) bytes of the same sizes
  *       (0 for most and for sizes that the call refuses, never more than
  *       128 MiB), 256-byte aligned, no initialisation needed.  Calls that may

@@ -201,3 +201,12 @@ def test_extension_is_built_again_for_another_pytorch(monkeypatch):
     monkeypatch.setattr(torch, "__version__", "1.0")
     build.build_binding()
     assert len(ran) == 1 and any("torch 1.0" in a for a in ran[0])
+
+
+def test_attention_of_too_many_sequences(lib):
+    """The time to find a block's sequence grows with their number: 65536 at most."""
+    most = {**ATTN, "B": 65536, "lse": ODD}                     # the lengths are taken, the next check is not
+    assert lib.w4a4_attention(*most.values()) == ALIGN
+    for B in (65537, 2 ** 20, 2 ** 24):
+        assert lib.w4a4_attention(*{**ATTN, "B": B, "lse": ODD}.values()) == SHAPE
+        assert lib.w4a4_attention_workspace_bytes(B, 2 ** 30, B, 8, 1, 128) == 0

@@ -72,6 +72,10 @@ namespace {
 
 constexpr int kTile = 128;             // query rows per MMA tile and keys per key tile
 constexpr int kFewRows = 32;           // query rows of a tile of few
+// Every block looks for its place among the sequences, so their search grows
+// with their square: 16384 single tokens x 8/8 heads take 25 ms, a million would
+// take minutes.
+constexpr int64_t kMaxSequences = 65536;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // log2: how far the maximum in use may fall behind, and how far below it the
@@ -941,7 +945,7 @@ extern "C" {
 // SPLIT: [chunks][Tq][Hq][D] fp32 partial outputs, [chunks][Tq][Hq] fp32 lse
 size_t w4a4_attention_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
   if (Tq <= 0 || Tk < 0 || B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || D < 1) return 0;
-  if (Tq > (int64_t(1) << 30) || Tk > (int64_t(1) << 30) || B > (int64_t(1) << 24) || Hq > 65535 || D > 128) return 0;
+  if (Tq > (int64_t(1) << 30) || Tk > (int64_t(1) << 30) || B > kMaxSequences || Hq > 65535 || D > 128) return 0;
   const Plan p = make_plan(Tq, Tk, B, Hq, Hk);
   if (p.chunk == 0) return 0;
   return static_cast<size_t>(p.chunks) * static_cast<size_t>(Tq) * static_cast<size_t>(Hq) * (D + 1) * 4;
@@ -956,7 +960,7 @@ int w4a4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
   if (Tq < 0 || Tk < 0 || Tq > (int64_t(1) << 30) || Tk > (int64_t(1) << 30)) return W4A4_ERR_SHAPE;
   if (Tq != 0 && (q == nullptr || out == nullptr)) return W4A4_ERR_NULL;
   if (Tk != 0 && (k == nullptr || v == nullptr)) return W4A4_ERR_NULL;
-  if (B < 1 || B > (int64_t(1) << 24)) return W4A4_ERR_SHAPE;
+  if (B < 1 || B > kMaxSequences) return W4A4_ERR_SHAPE;
   if ((cu_q == nullptr) != (cu_k == nullptr) || (cu_q == nullptr && B != 1)) return W4A4_ERR_NULL;
   if (D != 64 && D != 128) return W4A4_ERR_SHAPE;
   if (Hq < 1 || Hq > 65535 || Hk < 1 || Hq % Hk != 0) return W4A4_ERR_SHAPE;
