@@ -325,7 +325,8 @@ int w4a4_quantize_weight_w4a16(const float* W, int64_t N, int64_t K, int64_t ldw
  *       (offset may be NULL), bias [N] dtype or NULL: contiguous, from
  *       w4a4_quantize_weight_w4a16 or any other quantiser; all 16 codes of a
  *       nibble are valid (two's complement, -8..7)
- *   y [M, N] dtype output, row stride ldy >= N (no alignment rule)
+ *   y [M, N] dtype output, row stride ldy >= N (no alignment rule), no overlap
+ *       with the inputs
  *   0 <= M <= 64 (M == 0 is a no-op), N >= 1, 32 <= K <= 131072, K % 32 == 0,
  *   K % group == 0, group in {32, 64, 128}
  * The result does not depend on what else runs (no atomics); a row's result

@@ -4,6 +4,10 @@ activation, qk_norm_rope, attention over packed sequences, the W4A4 output
 linear.  Every stage is checked against its definition on the tensors that the
 run itself hands to it, and the whole is replayed from a graph."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -169,3 +173,59 @@ def test_small_layers_between_attentions(cuda_lib):
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want * 5)) and w4.last_device_error() == 0
+
+
+FIRST_CALL = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import w4a4_hadamard_rotated_b200 as w4
+
+gen = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)
+q, k, v, x = r(300, 8, 128), r(300, 2, 128), r(300, 2, 128), r(3, 256)
+codes, scale = torch.randint(-128, 128, (500, 128), generator=gen, device="cuda", dtype=torch.int8), r(500, 4)
+freq, axis = w4.rotary_frequencies((128,))
+pos = torch.arange(300, device="cuda")
+copies = [torch.empty_like(t) for t in (q, k, x)]
+side = torch.cuda.Stream()
+torch.cuda.synchronize()
+
+
+def block():
+    # copies and fills before each kernel, and a branch that joins
+    for c, t in zip(copies, (q, k, x)):
+        c.copy_(t)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y = w4.linear_w4a16(copies[2], codes, scale)
+    qr, kr = w4.qk_norm_rope(copies[0], copies[1], positions=pos, freq=freq, axis=axis)
+    out = torch.empty_like(q)
+    out.zero_()
+    w4.attention(qr, kr, v, causal=True, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    o2 = w4.attention(qr[:3], kr, v)
+    return y, qr, kr, out, o2
+
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = block()
+for c in copies:
+    c.fill_(7)
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+want = block()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and w4.last_device_error() == 0
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture(cuda_lib):
+    """In a process that has not called the library yet: each entry's first
+    call captured into a graph, behind copies, fills and a joined branch."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(w4.__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root)], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
