@@ -48,10 +48,12 @@
 //     tile instead of the other 96 rows; the MMAs still run over 128 rows, those
 //     behind the 32 of whatever lies there and read by nobody (8 tokens over 66796
 //     keys: 51 us; with 128 rows, four warps and two tiles 58).
-// Measured (bf16, D 128, graph replays): 4608 x 24 heads 220 us, 1.18 PF/s;
-// 32760 x 10 heads 4.63 ms, 1.16 PF/s (the board's power limit holds the clock
-// at 1.75 GHz); eight causal prompts, 11168 tokens x 40/8 heads, fp16 381 us,
-// 0.9 PF/s; 8 tokens x 32/8 heads over 66796 keys 51 us, 5.4 TB/s.
+// Measured (D 128, calls back to back for seconds, where the board's power limit
+// of 1000 W holds the clock at 1.6 to 1.75 GHz; in parentheses the first 10 ms of a
+// rested GPU): bf16, 4608 x 24 heads 249 us, 1.05 PF/s (215 us, 1.21); 32760 x 10
+// heads 4.73 ms, 1.16 PF/s (4.09, 1.35); fp16, eight causal prompts, 11168 tokens x
+// 40/8 heads 438 us, 0.78 PF/s (384, 0.89); bf16, 8 tokens x 32/8 heads over 66796
+// keys 57 us, 4.8 TB/s (52, 5.2).
 //   Every wait is bounded; an expired wait records W4A4_ERR_TIMEOUT, every
 //   role stops, copies and MMAs drain and tensor memory is freed.
 #include <cuda.h>
@@ -842,7 +844,10 @@ Plan make_plan(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hk) {
     if (p.few) {
       // Caches differ in length and the longest one ends last: where a join
       // costs little beside the rest, what is twice the average is cut too (a
-      // cache of 32769 and 39 of 500: 70 us, whole 410; 64 of 2001: 96 and 88)
+      // cache of 32769 and 39 of 500, a query each, 8/8 heads: 70 us, whole 410;
+      // 64 of 2001: 96 and 88).  The estimate is that of alike sequences: below
+      // 30 us a long one stays whole (the same caches, 32/4 heads: 388 us), as it
+      // does in batches of more rows (five queries each: 411 us)
       if (chunk == 0 && least > 30.f) chunk = 2 * each < 16 ? 16 : 2 * each;
       if (chunk != 0 && chunk * room < tiles) chunk = room == 0 ? tiles : (tiles + room - 1) / room;
     }

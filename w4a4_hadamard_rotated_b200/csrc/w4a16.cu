@@ -31,7 +31,8 @@
 //     the operand reads are free of bank conflicts; what is out of range
 //     arrives as zeros), one lane issuing, no barrier between warps.
 // Measured (graph replays): 1 x 3072 -> 3072 4.4 us, 1 x 5120 -> 30720 26 us
-// (3.2 TB/s, the widening's issue slots), 8 x 12288 -> 3072 with offsets 11.3 us,
+// (3.2 TB/s; issue slots 55% and ALU 53% busy: each warp's chain of wait, read,
+// widen and multiply, and four rounds for 3.24), 8 x 12288 -> 3072 with offsets 11.3 us,
 // 16 x 5120 -> 13824 of groups of 32 25.6 us.
 //   Every wait is bounded; an expired one records W4A4_ERR_TIMEOUT, ends the
 //   warp's sums early and lets its copies land.
